@@ -1,8 +1,10 @@
-"""Build the CUDA library in-tree: io_aware_exact_fa2_gb300/libfa2_gb300.so.
+"""Build the CUDA libraries in-tree: io_aware_exact_fa2_gb300/libfa2_gb300.so (the
+dense passes, include/fa2.h) and libfa2_cache_gb300.so (the 8-bit cache,
+include/fa2_cache.h).
 
 nvcc compiles each translation unit in csrc/ for sm_103a (in parallel), then
-links a shared library with the CUDA runtime linked statically and only the
-``fa2_*`` C symbols exported (a linker version script), so the library never
+links the shared libraries with the CUDA runtime linked statically and only the
+``fa2_*`` C symbols exported (a linker version script), so a library never
 interposes on, or binds to, another copy of the CUDA runtime in the process.
 
     python -m io_aware_exact_fa2_gb300.build [--force] [--verbose]
@@ -26,6 +28,11 @@ LIB_NAME = "libfa2_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["fa2_api.cu", "fa2_noalloc.cu", "fa2_fwd_d64.cu", "fa2_fwd_d128.cu", "fa2_fwd_d256.cu",
            "fa2_fwd_fp8_d128.cu", "fa2_bwd.cu"]
+# the 8-bit cache is a library of its own, so that the dense one's boundary stays what fa2.h declares
+CACHE_LIB_NAME = "libfa2_cache_gb300.so"
+CACHE_LIB_PATH = os.path.join(PKG, CACHE_LIB_NAME)
+CACHE_SOURCES = ["fa2_cache_api.cu", "fa2_cache_move.cu", "fa2_cache_attn_d64.cu", "fa2_cache_attn_d128.cu",
+                 "fa2_cache_attn_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fPIC,-fvisibility=hidden", "-Xptxas", "-v",
@@ -40,14 +47,15 @@ def nvcc() -> str:
 
 
 def source_digest() -> str:
-    """Hash of every kernel/host source and the public header (for staleness checks)."""
+    """Hash of every kernel/host source and the public headers (for staleness checks)."""
     h = hashlib.sha256()
     files = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
     for f in files:
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())
-    with open(os.path.join(INCLUDE, "fa2.h"), "rb") as fh:
-        h.update(fh.read())
+    for f in ("fa2.h", "fa2_cache.h"):
+        with open(os.path.join(INCLUDE, f), "rb") as fh:
+            h.update(fh.read())
     return h.hexdigest()[:16]
 
 
@@ -74,7 +82,7 @@ def _stamp_path() -> str:
 
 
 def is_fresh() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(_stamp_path()):
+    if not all(os.path.exists(p) for p in (LIB_PATH, CACHE_LIB_PATH, _stamp_path())):
         return False
     with open(_stamp_path()) as fh:
         return fh.read().strip() == source_digest()
@@ -94,24 +102,8 @@ def _compile(src: str, verbose: bool, build_dir: str, extra_flags) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str | None = None,
-          build_dir: str | None = None) -> str:
-    """Compile and link the library unless it is already up to date. Returns its path.
-
-    extra_flags / lib_path / build_dir build a separate copy (e.g. with -D tile
-    overrides for tuning) without touching the in-tree library.
-    """
-    default = lib_path is None and not extra_flags
-    if default and not force and is_fresh():
-        return LIB_PATH
-    out = LIB_PATH if lib_path is None else lib_path
-    bdir = BUILD if build_dir is None else build_dir
-    os.makedirs(bdir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose, bdir, tuple(extra_flags)), SOURCES))
+def _link(objs, out: str, bdir: str) -> None:
     vscript = os.path.join(bdir, "exports.map")
-    with open(vscript, "w") as fh:
-        fh.write("{\n  global: fa2_*;\n  local: *;\n};\n")
     tmp = out + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
            "-Xlinker", f"--version-script={vscript}", "-Xlinker", "-Bsymbolic"]
@@ -119,7 +111,30 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str | None = None,
+          build_dir: str | None = None) -> str:
+    """Compile and link the libraries unless they are already up to date. Returns the path
+    of the dense one.
+
+    extra_flags / lib_path / build_dir build a separate copy of the dense library (e.g.
+    with -D tile overrides for tuning) without touching the in-tree ones.
+    """
+    default = lib_path is None and not extra_flags
+    if default and not force and is_fresh():
+        return LIB_PATH
+    out = LIB_PATH if lib_path is None else lib_path
+    bdir = BUILD if build_dir is None else build_dir
+    os.makedirs(bdir, exist_ok=True)
+    sources = SOURCES + (CACHE_SOURCES if default else [])
+    with cf.ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = list(ex.map(lambda s: _compile(s, verbose, bdir, tuple(extra_flags)), sources))
+    with open(os.path.join(bdir, "exports.map"), "w") as fh:
+        fh.write("{\n  global: fa2_*;\n  local: *;\n};\n")
+    _link(objs[:len(SOURCES)], out, bdir)
     if default:
+        _link(objs[len(SOURCES):], CACHE_LIB_PATH, bdir)
         with open(_stamp_path(), "w") as fh:
             fh.write(source_digest())
     return out
