@@ -221,7 +221,8 @@ __device__ __forceinline__ void load_rows(Rows<C> &w, const AttnArgs &a, const S
             other = __shfl_xor_sync(0xffffffffu, top, 2);
             top = top > other ? top : other;
             // a row with an infinity or NaN has no finite scores: make it NaN
-            const int e = static_cast<int>(top >> 7) - 127 - 14;
+            int e = static_cast<int>(top >> 7) - 127 - 14;
+            e = e < -126 ? -126 : e;   // 2^126 is as far as fp32 goes (zero and subnormal rows)
             w.e[mt][half] = e;
             const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
 #pragma unroll
@@ -281,6 +282,8 @@ __device__ __forceinline__ void consume(Rows<C> &w, uint32_t kv, const uint8_t *
                                         float scale_log2, int g, int t)
 {
     constexpr int D = C::D, MT = C::MT;
+    const bool nan_scale = ev == 128;   // (that of the keys: below)
+    ev = nan_scale ? 0 : ev;
     float s[MT][2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
@@ -309,7 +312,7 @@ __device__ __forceinline__ void consume(Rows<C> &w, uint32_t kv, const uint8_t *
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const float f = scale_log2 * pow2i(w.e[mt][half] + ek);
+            const float f = ek == 128 ? __uint_as_float(0x7fc00000u) : scale_log2 * pow2i(w.e[mt][half] + ek);
             float x = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
@@ -414,6 +417,15 @@ __device__ __forceinline__ void consume(Rows<C> &w, uint32_t kv, const uint8_t *
     }
     if (!whole && __any_sync(0xffffffffu, nan))
         nan_values<C>(w, v_ptr, pos0, t);
+    if (nan_scale)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (w.lo[mt][half] < pos0 + CHUNK && w.hi[mt][half] > pos0)   // the row sees one of the keys
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j)
+                        w.o[mt][j][half * 2] = w.o[mt][j][half * 2 + 1] = __uint_as_float(0x7fc00000u);
 }
 
 // One CTA's share of the line of tiles.

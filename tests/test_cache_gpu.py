@@ -264,15 +264,16 @@ def test_missing_pages_are_not_seen(D, Lq):
 @pytest.mark.parametrize("Lq", [1, 6, 90])
 def test_nan_and_infinity_reach_only_rows_that_see_them(D, Lq):
     """NaN codes and NaN scales in keys and values; rows behind them are NaN, earlier ones untouched."""
-    lens = [120, 120, 120, 120]
-    c = Cache(4, 1, D, 16, lens, seed=D + 2)
+    lens = [120, 120, 120, 120, 120]
+    c = Cache(5, 1, D, 16, lens, seed=D + 2)
     pos = 117
     page, slot = c.table[:, pos // 16], pos % 16
     c.k[page[0], 0, slot, 5] = 0x7f
     c.v[page[1], 0, slot, 9] = 0xff
     c.v[page[1], 0, slot - 1, D - 1] = 0x7f
     c.ks[c.table[2, 7], 0] = 255
-    q = ref.bf16(c.rng.standard_normal((4, 3, Lq, D)))
+    c.vs[c.table[4, 7], 0] = 255
+    q = ref.bf16(c.rng.standard_normal((5, 3, Lq, D)))
     q[3, 1, 0, 2] = float("inf")
     q[3, 2, Lq - 1, 0] = float("nan")
     attend(c, 3, Lq, lens, q=q)
