@@ -154,6 +154,22 @@ fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o, float *lse
  */
 fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq, int D, int device, size_t *bytes);
 
+/*
+ * fa2_cache_get_device_error -- synchronises `stream`, then reads and clears this
+ * library's device-side error word on the current device, as fa2_get_device_error
+ * does for the dense passes: every wait between warps in the attention kernels is
+ * bounded (one second; FA2_WAIT_LIMIT_MS), one that runs out records a code, and the
+ * kernel winds down.  Outputs of that call are then undefined, and a workspace it used
+ * must be zero-filled again.
+ *
+ *   detail   optional: the raw code (0 = none), the waiting role in bits 8-11 (8
+ *            softmax, 9 conversion, 10 MMA issuer, 11 a CTA's final wait for its
+ *            own work), the barrier in the low byte.
+ *
+ * Returns FA2_OK, FA2_ERR_TIMEOUT, or FA2_ERR_CUDA.
+ */
+fa2_status fa2_cache_get_device_error(void *stream, int *detail);
+
 #ifdef __cplusplus
 }
 #endif

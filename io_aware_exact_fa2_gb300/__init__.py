@@ -21,7 +21,7 @@ _BINDING_NAMES = (
 
 _CACHE_NAMES = (
     "fa2_cache_write", "fa2_cache_read", "fa2_cache_attn", "fa2_cache_attn_workspace_size",
-    "fa2_cache_attn_workspace", "cache_library_path", "load_cache_library",
+    "fa2_cache_attn_workspace", "fa2_cache_get_device_error", "cache_library_path", "load_cache_library",
 )
 
 

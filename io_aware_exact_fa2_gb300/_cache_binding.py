@@ -40,6 +40,8 @@ def load_cache_library() -> ctypes.CDLL:
     lib.fa2_cache_attn.argtypes = [c, _vp, _vp, _vp, ll3, ll3, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _vp, sz, _vp]
     lib.fa2_cache_attn_workspace_size.restype = _i
     lib.fa2_cache_attn_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i, ctypes.POINTER(sz)]
+    lib.fa2_cache_get_device_error.restype = _i
+    lib.fa2_cache_get_device_error.argtypes = [_vp, ctypes.POINTER(_i)]
     return lib
 
 
@@ -181,3 +183,10 @@ def fa2_cache_attn_workspace(q, k_cache):
     B, Hq, Lq, D = q.shape
     n = fa2_cache_attn_workspace_size(B, Hq, k_cache.shape[1], Lq, D, q.device.index or 0)
     return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def fa2_cache_get_device_error(stream=None) -> tuple[int, int]:
+    """Synchronise, then read and clear the cache kernels' error word: (status, raw code)."""
+    detail = ctypes.c_int(0)
+    st = _lib.fa2_cache_get_device_error(_stream_handle(stream, torch.cuda.current_device()), ctypes.byref(detail))
+    return st, detail.value

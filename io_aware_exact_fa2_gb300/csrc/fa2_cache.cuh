@@ -46,6 +46,8 @@ struct AttnArgs {
     void *workspace;
     size_t workspace_bytes;
     int num_sms;
+    int *err;                       // device error word
+    unsigned long long wait_limit_ns;
     cudaStream_t stream;
 };
 
@@ -117,6 +119,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// e4m3 NaN codes of four as zeros.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w)
+{
+    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // high bit of each NaN's byte
+    return w & ~((nan >> 7) * 0xffu);
 }
 
 // Page that entry `j` of sequence b's table names, or -1.

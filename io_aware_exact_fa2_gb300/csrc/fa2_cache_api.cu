@@ -2,6 +2,7 @@
 // device selection, dispatch.
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 
 #include "fa2_cache.cuh"
@@ -10,6 +11,10 @@
 
 namespace fa2 {
 namespace cache {
+
+// Written by a kernel when one of its bounded waits runs out (first code wins).
+static __device__ int g_cache_error;
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -73,6 +78,35 @@ int sm_count(int dev)
     if (dev >= 0 && dev < kMaxDevices)
         cache[dev] = n;
     return n;
+}
+
+// Device address of g_cache_error on `dev`, which must be current (looked up once per device).
+int *device_error_ptr(int dev)
+{
+    static std::mutex mu;
+    static int *cache[kMaxDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < kMaxDevices && cache[dev])
+        return cache[dev];
+    void *ptr = nullptr;
+    if (cudaGetSymbolAddress(&ptr, g_cache_error) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return nullptr;
+    }
+    if (dev >= 0 && dev < kMaxDevices)
+        cache[dev] = static_cast<int *>(ptr);
+    return static_cast<int *>(ptr);
+}
+
+// Limit of the kernels' waits between warps (FA2_WAIT_LIMIT_MS, read once).
+unsigned long long wait_limit_ns()
+{
+    static const unsigned long long limit = [] {
+        const char *s = std::getenv("FA2_WAIT_LIMIT_MS");
+        const long long ms = s ? std::atoll(s) : 0;
+        return static_cast<unsigned long long>(ms > 0 ? ms : 1000) * 1000000ull;
+    }();
+    return limit;
 }
 
 // (batch, head, row) element strides of a bf16 [B, H, L, D] view; NULL: contiguous.
@@ -238,7 +272,9 @@ FA2_EXPORT fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o,
     if (dev.status() != FA2_OK)
         return dev.status();
     a.num_sms = fa2::cache::sm_count(dev.id());
-    if (a.num_sms <= 0)
+    a.err = fa2::cache::device_error_ptr(dev.id());
+    a.wait_limit_ns = fa2::cache::wait_limit_ns();
+    if (a.num_sms <= 0 || !a.err)
         return FA2_ERR_CUDA;
     return c->D == 64 ? fa2::cache::launch_attn_d64(a)
                       : c->D == 128 ? fa2::cache::launch_attn_d128(a) : fa2::cache::launch_attn_d256(a);
@@ -261,4 +297,26 @@ FA2_EXPORT fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq
         return FA2_ERR_CUDA;
     *bytes = fa2::cache::workspace_bytes(D, static_cast<long long>(Lq) * (Hq / H), sms);
     return FA2_OK;
+}
+
+FA2_EXPORT fa2_status fa2_cache_get_device_error(void *stream, int *detail)
+{
+    if (detail)
+        *detail = 0;
+    int v = 0;
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&v, fa2::cache::g_cache_error, sizeof v) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return FA2_ERR_CUDA;
+    }
+    if (v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(fa2::cache::g_cache_error, &zero, sizeof zero) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return FA2_ERR_CUDA;
+        }
+    }
+    if (detail)
+        *detail = v;
+    return v ? FA2_ERR_TIMEOUT : FA2_OK;
 }

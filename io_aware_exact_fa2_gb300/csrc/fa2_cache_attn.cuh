@@ -27,16 +27,12 @@
 #pragma once
 
 #include <atomic>
-#include <climits>
 
-#include "fa2_cache.cuh"
+#include "fa2_cache_line.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa2 {
 namespace cache {
-
-constexpr int CHUNK = 16;                 // keys a warp takes at a time; divides every page size
-constexpr int MIN_TILES = 4;              // least tiles a CTA's range is cut down to
 
 template <int D_, int MT_>
 struct AttnCfg {
@@ -54,26 +50,6 @@ struct AttnCfg {
     static constexpr int SMEM_BYTES = NW * RING_BYTES;
     static_assert(RING_BYTES >= R * D * 4, "a warp's partial O lies in its ring");
 };
-
-// Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
-// R rows: O [R, D] fp32, then the log2-sum-exp2 [R].
-struct Parts {
-    int *counters;      // [grid]
-    float *data;
-    __host__ __device__ static constexpr size_t slot_floats(int R, int D) { return static_cast<size_t>(R) * (D + 1); }
-    __host__ __device__ static constexpr size_t counter_bytes(int grid)
-    {
-        return (static_cast<size_t>(grid) * sizeof(int) + 255) & ~static_cast<size_t>(255);
-    }
-};
-
-// Bytes of workspace for units of R rows of D.
-template <class C>
-size_t attn_workspace(int num_sms)
-{
-    return Parts::counter_bytes(num_sms * C::CTAS) +
-           static_cast<size_t>(num_sms) * C::CTAS * 2 * Parts::slot_floats(C::R, C::D) * sizeof(float);
-}
 
 #ifdef __CUDACC__
 
@@ -122,52 +98,6 @@ __device__ __forceinline__ uint32_t chunk_offset(int row, int col)
     const int line = D == 128 ? row : row * 2 + (col >> 3);
     const int x = V ? row & 6 : ((row & 1) << 2) | ((row >> 1) & 3);
     return line * 128 + (((col & 7) ^ x) << 4);
-}
-
-// Keys that a block of query rows sees at all: [lo, hi), and the tiles they span.
-struct Span {
-    int lo, hi, tiles;
-};
-
-struct Seq {
-    int kv, n;      // positions held, query rows of them
-};
-
-__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
-{
-    Seq s;
-    const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-    const int kv = a.kv_lens[b];
-    s.kv = kv < 0 ? 0 : kv > cap ? static_cast<int>(cap) : kv;
-    const int n = a.q_lens ? a.q_lens[b] : a.Lq;
-    s.n = n < 0 ? 0 : n > a.Lq ? a.Lq : n;
-    return s;
-}
-
-template <class C>
-__device__ __forceinline__ Span span_of(const AttnArgs &a, const Seq &s, int rb)
-{
-    const int rows = s.n * a.G;
-    const int r1 = (rb + 1) * C::R < rows ? (rb + 1) * C::R : rows;
-    const int i0 = rb * C::R / a.G, i1 = (r1 - 1) / a.G;
-    Span p;
-    p.hi = a.causal ? s.kv - s.n + i1 + 1 : s.kv;
-    p.hi = p.hi < 0 ? 0 : p.hi;
-    p.lo = 0;
-    if (a.window >= 0) {
-        const long long lo = static_cast<long long>(s.kv) - s.n + i0 - a.window;
-        p.lo = lo > 0 ? static_cast<int>(lo) : 0;
-    }
-    const int from = p.lo & ~(CHUNK - 1);
-    p.tiles = p.hi > from ? (p.hi - from + C::TILE - 1) / C::TILE : 0;
-    p.tiles = p.tiles > 0 ? p.tiles : 1;   // a unit that sees nothing still writes its rows
-    return p;
-}
-
-template <class C>
-__device__ __forceinline__ int row_blocks(const AttnArgs &a, const Seq &s)
-{
-    return (s.n * a.G + C::R - 1) / C::R;
 }
 
 // Everything a warp knows of its rows: row mt * 16 + g + 8 * half of the unit for
@@ -267,13 +197,6 @@ __device__ __forceinline__ void nan_values(Rows<C> &w, const uint8_t *v, int pos
                             w.o[mt][n][half * 2 + k] = __uint_as_float(0x7fc00000u);
                     }
             }
-}
-
-// e4m3 NaN codes of four as zeros.
-__device__ __forceinline__ uint32_t without_nan(uint32_t w)
-{
-    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // high bit of each NaN's byte
-    return w & ~((nan >> 7) * 0xffu);
 }
 
 // 16 keys and values in shared memory, at positions pos0 .. pos0 + 15.
@@ -428,15 +351,6 @@ __device__ __forceinline__ void consume(Rows<C> &w, uint32_t kv, const uint8_t *
                         w.o[mt][j][half * 2] = w.o[mt][j][half * 2 + 1] = __uint_as_float(0x7fc00000u);
 }
 
-// One CTA's share of the line of tiles.
-struct Range {
-    long long total;    // tiles of all units
-    int grid;           // ranges
-    __device__ long long begin(int c) const { return total * c / grid; }
-    // the range that tile x lies in
-    __device__ int owner(long long x) const { return static_cast<int>(((x + 1) * grid + total - 1) / total - 1); }
-};
-
 // Where the D / 4 four-float units of a row lie in a warp's partial O [R, D]: the lanes
 // that store (row g, 32 or 16 consecutive d each) meet all banks.
 template <int D>
@@ -454,103 +368,18 @@ __global__ void __launch_bounds__(C::T, C::CTAS) attn_kernel(const AttnArgs a, c
 {
     constexpr int D = C::D, R = C::R, NW = C::NW, ST = C::ST;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long sh_scan[NW];
-    __shared__ long long sh_off;
-    __shared__ int sh_b;
+    __shared__ LineShared sh_line;
     __shared__ float sh_m[NW][R], sh_l[NW][R];
     __shared__ float sh_lse[R];
     __shared__ int sh_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-
-    // ---- the line of tiles: for each sequence all heads, for each head its row blocks.
-    // A thread sums a run of sequences; the one whose run holds this CTA's first tile
-    // finds the sequence.
-    const int per = (a.c.B + C::T - 1) / C::T;
-    const int b0 = tid * per, b1 = b0 + per < a.c.B ? b0 + per : a.c.B;
-    long long mine = 0;
-    auto tiles_of = [&](const Seq &s) {
-        long long n = 0;
-        const int blocks = row_blocks<C>(a, s);
-        for (int rb = 0; rb < blocks; ++rb)
-            n += span_of<C>(a, s, rb).tiles;
-        return n;
-    };
-    for (int b = b0; b < b1; ++b)
-        mine += tiles_of(sequence(a, b)) * a.c.H;
-    long long upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, d);
-        upto += lane >= d ? x : 0;
-    }
-    if (lane == 31)
-        sh_scan[warp] = upto;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        before += w < warp ? sh_scan[w] : 0;
-        total += sh_scan[w];
-    }
-    before += upto - mine;
-    if (total == 0)
-        return;
     const bool cut = parts.data != nullptr;
-    Range range;
-    range.total = total;
-    {
-        const long long most = cut ? (total + MIN_TILES - 1) / MIN_TILES : total;
-        range.grid = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-    }
     const int cta = blockIdx.x;
-    if (cta >= range.grid)
-        return;
-    const long long first = range.begin(cta), end = range.begin(cta + 1);
-    if (first >= end)
-        return;
-    if (first >= before && first < before + mine) {
-        long long at = before;
-        int b = b0;
-        for (;; ++b) {
-            const long long n = tiles_of(sequence(a, b)) * a.c.H;
-            if (first < at + n)
-                break;
-            at += n;
-        }
-        sh_b = b;
-        sh_off = at;
-    }
-    __syncthreads();
-
-    // ---- walk the units that this range meets
-    int b = sh_b;
-    long long at = sh_off;               // the line's tile at which the unit below begins
-    Seq s = sequence(a, b);
-    const long long per_head = tiles_of(s);
-    int h = static_cast<int>((first - at) / per_head), rb = 0;
-    at += h * per_head;
-    Span span = span_of<C>(a, s, 0);
-    auto next = [&]() -> bool {          // the following unit; false at the line's end
-        at += span.tiles;
-        if (++rb == row_blocks<C>(a, s)) {
-            rb = 0;
-            if (++h == a.c.H) {
-                h = 0;
-                do {
-                    if (++b == a.c.B)
-                        return false;
-                    s = sequence(a, b);
-                } while (s.n == 0);
-            }
-        }
-        span = span_of<C>(a, s, rb);
-        return true;
-    };
-    while (at + span.tiles <= first)
-        if (!next())
-            return;
-    if (!cut && at < first && !next())   // uncut: a unit belongs to the range its first tile lies in
+    Range range;
+    long long first, end;
+    Line<C> line;
+    if (!find_range<C>(a, cut, sh_line, range, first, end, line))
         return;
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING_BYTES;
@@ -559,21 +388,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS) attn_kernel(const AttnArgs a, c
     const float scale_log2 = a.scale * 1.4426950408889634f;
     Rows<C> w;
 
-    while (at < end) {
-        const long long unit_at = at;
-        const int tile0 = cut && first > at ? static_cast<int>(first - at) : 0;
-        const int tile1 = cut && end < at + span.tiles ? static_cast<int>(end - at) : span.tiles;
+    for (;;) {
+        const int b = line.b, h = line.h, rb = line.rb;
+        const Seq s = line.s;
+        const Span span = line.span;
+        const int tile0 = cut && first > line.at ? static_cast<int>(first - line.at) : 0;
+        const int tile1 = cut && end < line.at + span.tiles ? static_cast<int>(end - line.at) : span.tiles;
         load_rows<C>(w, a, s, b, h, rb, g, t);
-        // keys that every row of the block sees
         int all_lo, all_hi;
-        {
-            const int rows = s.n * a.G;
-            const int r1 = (rb + 1) * R < rows ? (rb + 1) * R : rows;
-            const int i0 = rb * R / a.G, i1 = (r1 - 1) / a.G;
-            all_hi = a.causal ? s.kv - s.n + i0 + 1 : s.kv;
-            const long long lo = static_cast<long long>(s.kv) - s.n + i1 - a.window;
-            all_lo = a.window >= 0 && lo > 0 ? static_cast<int>(lo) : 0;
-        }
+        line.seen_by_all(a, all_lo, all_hi);
         const int from = span.lo & ~(CHUNK - 1);
         // this warp's chunks: number k at position chunk0 + k * TILE
         const int chunk0 = from + tile0 * C::TILE + warp * CHUNK;
@@ -682,8 +505,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS) attn_kernel(const AttnArgs a, c
                     sh_lse[r] = l == 0.f ? -INFINITY : m + ptx::lg2_approx(l);
             }
         __syncthreads();
-        const int c0 = cut ? range.owner(unit_at) : cta;
-        const int c1 = cut ? range.owner(unit_at + span.tiles - 1) : cta;
+        const int c0 = cut ? range.owner(line.at) : cta;
+        const int c1 = cut ? range.owner(line.at + span.tiles - 1) : cta;
         const int rows = s.n * a.G;
         auto write_o = [&](int r, int u, const float4 &v) {   // unit u of row r
             const int rr = rb * R + r;
@@ -727,33 +550,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS) attn_kernel(const AttnArgs a, c
             __syncthreads();
             if (sh_last) {   // every part of the unit is there: merge them in key order
                 __threadfence();
-                auto slot = [&](int c) { return parts.data + (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * slot_floats; };
-                for (int i = tid; i < R * (D / 4); i += C::T) {
-                    const int r = i / (D / 4), u = i % (D / 4);
-                    float top = -INFINITY;
-                    for (int c = c0; c <= c1; ++c)
-                        top = fmaxf(top, __ldcg(slot(c) + R * D + r));
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float l = 0.f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float f = ptx::ex2_approx(__ldcg(slot(c) + R * D + r) - ref);
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot(c)) + i);
-                        l += f;
-                        v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
-                    }
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-                    write_o(r, u, v);
-                    if (u == 0)
-                        write_lse(r, l == 0.f ? -INFINITY : ref + ptx::lg2_approx(l));
-                }
+                merge_parts<C>(parts, c0, c1, tid, C::T, write_o, write_lse);
                 if (tid == 0)
                     parts.counters[c0] = 0;
             }
         }
         __syncthreads();   // the rings and sh_* are free again
-        if (!next())
+        if (!line.next(a) || line.at >= end)
             break;
     }
 }
@@ -761,25 +564,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS) attn_kernel(const AttnArgs a, c
 template <class C>
 fa2_status launch_attn(const AttnArgs &a)
 {
-    // workspace: counters, then the parts
-    const int grid_max = a.num_sms * C::CTAS;
-    Parts parts{nullptr, nullptr};
-    if (a.workspace) {
-        if (a.workspace_bytes < attn_workspace<C>(a.num_sms))
-            return FA2_ERR_INVALID_ARG;
-        parts.counters = static_cast<int *>(a.workspace);
-        parts.data = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + Parts::counter_bytes(grid_max));
-    }
-    // no more CTAs than the longest sequences could make tiles for
-    const long long blocks = (static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R;
-    const long long tiles = ((static_cast<long long>(a.c.max_pages) << a.c.page_shift) + C::TILE - 1) / C::TILE + 1;
-    long long grid = parts.data ? (tiles + MIN_TILES - 1) / MIN_TILES : 1;
-    grid = grid > grid_max ? grid_max : grid;
-    grid *= blocks > grid_max ? grid_max : blocks;
-    grid = grid > grid_max ? grid_max : grid;
-    grid *= static_cast<long long>(a.c.B) * a.c.H;
-    grid = grid > grid_max ? grid_max : grid;
-
+    Parts parts;
+    if (!parts_of<C>(a, parts))
+        return FA2_ERR_INVALID_ARG;
+    const int grid = line_grid<C>(a, parts.data != nullptr);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
         return FA2_ERR_CUDA;
@@ -792,7 +580,7 @@ fa2_status launch_attn(const AttnArgs &a)
         }
         configured.fetch_or(bit);
     }
-    attn_kernel<C><<<static_cast<unsigned>(grid), C::T, C::SMEM_BYTES, a.stream>>>(a, parts);
+    attn_kernel<C><<<grid, C::T, C::SMEM_BYTES, a.stream>>>(a, parts);
     return cudaGetLastError() == cudaSuccess ? FA2_OK : FA2_ERR_CUDA;
 }
 #endif

@@ -1,0 +1,283 @@
+// fa2_cache_line.cuh -- how fa2_cache_attn's kernels share out their work: the key tiles
+// of all sequences, heads and blocks of query rows as one line, cut into equal ranges.
+//
+// A unit is a block of C::R query rows of one (sequence, key/value head); it spans the
+// tiles of C::TILE keys that any of its rows sees.  Units lie on the line in the order
+// sequence, head, row block, so that CTAs that run side by side read the same keys.
+// Lengths are device data, so every CTA lays out the line for itself.
+#pragma once
+
+#include "fa2_cache.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa2 {
+namespace cache {
+
+constexpr int CHUNK = 16;                 // keys of the smallest piece; divides every page size
+constexpr int MIN_TILES = 4;              // least tiles a CTA's range is cut down to
+
+// Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
+// R rows: O [R, D] fp32, then the log2-sum-exp2 [R].
+struct Parts {
+    int *counters;      // [grid]
+    float *data;
+    __host__ __device__ static constexpr size_t slot_floats(int R, int D) { return static_cast<size_t>(R) * (D + 1); }
+    __host__ __device__ static constexpr size_t counter_bytes(int grid)
+    {
+        return (static_cast<size_t>(grid) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+    }
+};
+
+// Bytes of workspace for units of R rows of D.
+template <class C>
+size_t attn_workspace(int num_sms)
+{
+    return Parts::counter_bytes(num_sms * C::CTAS) +
+           static_cast<size_t>(num_sms) * C::CTAS * 2 * Parts::slot_floats(C::R, C::D) * sizeof(float);
+}
+
+// The workspace as parts (none: null pointers); false if it is too small.
+template <class C>
+bool parts_of(const AttnArgs &a, Parts &parts)
+{
+    parts = Parts{nullptr, nullptr};
+    if (!a.workspace)
+        return true;
+    if (a.workspace_bytes < attn_workspace<C>(a.num_sms))
+        return false;
+    parts.counters = static_cast<int *>(a.workspace);
+    parts.data = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + Parts::counter_bytes(a.num_sms * C::CTAS));
+    return true;
+}
+
+// CTAs to launch: no more than the longest sequences could make ranges for.
+template <class C>
+int line_grid(const AttnArgs &a, bool cut)
+{
+    const long long most = a.num_sms * C::CTAS;
+    const long long blocks = (static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R;
+    const long long tiles = ((static_cast<long long>(a.c.max_pages) << a.c.page_shift) + C::TILE - 1) / C::TILE + 1;
+    long long grid = cut ? (tiles + MIN_TILES - 1) / MIN_TILES : 1;
+    grid = grid > most ? most : grid;
+    grid *= blocks > most ? most : blocks;
+    grid = grid > most ? most : grid;
+    grid *= static_cast<long long>(a.c.B) * a.c.H;
+    return static_cast<int>(grid > most ? most : grid);
+}
+
+#ifdef __CUDACC__
+
+// Keys that a block of query rows sees at all: [lo, hi), and the tiles they span.
+struct Span {
+    int lo, hi, tiles;
+};
+
+struct Seq {
+    int kv, n;      // positions held, query rows of them
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
+{
+    Seq s;
+    const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
+    const int kv = a.kv_lens[b];
+    s.kv = kv < 0 ? 0 : kv > cap ? static_cast<int>(cap) : kv;
+    const int n = a.q_lens ? a.q_lens[b] : a.Lq;
+    s.n = n < 0 ? 0 : n > a.Lq ? a.Lq : n;
+    return s;
+}
+
+template <class C>
+__device__ __forceinline__ Span span_of(const AttnArgs &a, const Seq &s, int rb)
+{
+    const int rows = s.n * a.G;
+    const int r1 = (rb + 1) * C::R < rows ? (rb + 1) * C::R : rows;
+    const int i0 = rb * C::R / a.G, i1 = (r1 - 1) / a.G;
+    Span p;
+    p.hi = a.causal ? s.kv - s.n + i1 + 1 : s.kv;
+    p.hi = p.hi < 0 ? 0 : p.hi;
+    p.lo = 0;
+    if (a.window >= 0) {
+        const long long lo = static_cast<long long>(s.kv) - s.n + i0 - a.window;
+        p.lo = lo > 0 ? static_cast<int>(lo) : 0;
+    }
+    const int from = p.lo & ~(CHUNK - 1);
+    p.tiles = p.hi > from ? (p.hi - from + C::TILE - 1) / C::TILE : 0;
+    p.tiles = p.tiles > 0 ? p.tiles : 1;   // a unit that sees nothing still writes its rows
+    return p;
+}
+
+template <class C>
+__device__ __forceinline__ int row_blocks(const AttnArgs &a, const Seq &s)
+{
+    return (s.n * a.G + C::R - 1) / C::R;
+}
+
+// One CTA's share of the line of tiles.
+struct Range {
+    long long total;    // tiles of all units
+    int grid;           // ranges
+    __device__ long long begin(int c) const { return total * c / grid; }
+    // the range that tile x lies in
+    __device__ int owner(long long x) const { return static_cast<int>(((x + 1) * grid + total - 1) / total - 1); }
+};
+
+// Tiles of one head's units of a sequence.
+template <class C>
+__device__ __forceinline__ long long tiles_of(const AttnArgs &a, const Seq &s)
+{
+    long long n = 0;
+    const int blocks = row_blocks<C>(a, s);
+    for (int rb = 0; rb < blocks; ++rb)
+        n += span_of<C>(a, s, rb).tiles;
+    return n;
+}
+
+// A unit's place on the line.
+template <class C>
+struct Line {
+    long long at;      // its first tile
+    int b, h, rb;
+    Seq s;
+    Span span;
+
+    __device__ __forceinline__ bool next(const AttnArgs &a)   // the following unit; false at the line's end
+    {
+        at += span.tiles;
+        if (++rb == row_blocks<C>(a, s)) {
+            rb = 0;
+            if (++h == a.c.H) {
+                h = 0;
+                do {
+                    if (++b == a.c.B)
+                        return false;
+                    s = sequence(a, b);
+                } while (s.n == 0);
+            }
+        }
+        span = span_of<C>(a, s, rb);
+        return true;
+    }
+    // keys that every row of the block sees: [lo, hi)
+    __device__ __forceinline__ void seen_by_all(const AttnArgs &a, int &lo, int &hi) const
+    {
+        const int rows = s.n * a.G;
+        const int r1 = (rb + 1) * C::R < rows ? (rb + 1) * C::R : rows;
+        const int i0 = rb * C::R / a.G, i1 = (r1 - 1) / a.G;
+        hi = a.causal ? s.kv - s.n + i0 + 1 : s.kv;
+        const long long from = static_cast<long long>(s.kv) - s.n + i1 - a.window;
+        lo = a.window >= 0 && from > 0 ? static_cast<int>(from) : 0;
+    }
+};
+
+struct LineShared {
+    long long scan[32], off;
+    int b;
+};
+
+// Lays out the line and finds this CTA's range of it, [first, end), and the unit it
+// begins with; all C::T threads call it.  False: nothing to do.  Uncut (cut false), a
+// unit belongs whole to the range that its first tile lies in.
+template <class C>
+__device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShared &sh, Range &range, long long &first,
+                                           long long &end, Line<C> &line)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // a thread sums a run of sequences; the one whose run holds the first tile finds
+    // the sequence
+    const int per = (a.c.B + C::T - 1) / C::T;
+    const int b0 = tid * per, b1 = b0 + per < a.c.B ? b0 + per : a.c.B;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += tiles_of<C>(a, sequence(a, b)) * a.c.H;
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+        upto += lane >= d ? x : 0;
+    }
+    if (lane == 31)
+        sh.scan[warp] = upto;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < C::T / 32; ++w) {
+        before += w < warp ? sh.scan[w] : 0;
+        total += sh.scan[w];
+    }
+    before += upto - mine;
+    if (total == 0)
+        return false;
+    range.total = total;
+    const long long most = cut ? (total + MIN_TILES - 1) / MIN_TILES : total;
+    range.grid = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    const int cta = blockIdx.x;
+    if (cta >= range.grid)
+        return false;
+    first = range.begin(cta);
+    end = range.begin(cta + 1);
+    if (first >= end)
+        return false;
+    if (first >= before && first < before + mine) {
+        long long at = before;
+        int b = b0;
+        for (;; ++b) {
+            const long long n = tiles_of<C>(a, sequence(a, b)) * a.c.H;
+            if (first < at + n)
+                break;
+            at += n;
+        }
+        sh.b = b;
+        sh.off = at;
+    }
+    __syncthreads();
+    line.b = sh.b;
+    line.at = sh.off;
+    line.s = sequence(a, line.b);
+    const long long per_head = tiles_of<C>(a, line.s);
+    line.h = static_cast<int>((first - line.at) / per_head);
+    line.rb = 0;
+    line.at += line.h * per_head;
+    line.span = span_of<C>(a, line.s, 0);
+    while (line.at + line.span.tiles <= first)
+        if (!line.next(a))
+            return false;
+    if (!cut && line.at < first && !line.next(a))
+        return false;
+    return line.at < end;
+}
+
+// Merges the parts of a unit that ranges c0 .. c1 computed, always in that order, by
+// `threads` threads of which the caller is number `tid`; write(row, unit, value) takes
+// four values of O, write_lse(row, value) the log2-sum-exp2.
+template <class C, class W, class L>
+__device__ __forceinline__ void merge_parts(const Parts &parts, int c0, int c1, int tid, int threads, W write, L write_lse)
+{
+    constexpr int R = C::R, D = C::D;
+    const size_t slot_floats = Parts::slot_floats(R, D);
+    auto slot = [&](int c) { return parts.data + (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * slot_floats; };
+    for (int i = tid; i < R * (D / 4); i += threads) {
+        const int r = i / (D / 4), u = i % (D / 4);
+        float top = -INFINITY;
+        for (int c = c0; c <= c1; ++c)
+            top = fmaxf(top, __ldcg(slot(c) + R * D + r));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float f = ptx::ex2_approx(__ldcg(slot(c) + R * D + r) - ref);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot(c)) + i);
+            l += f;
+            v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+        write(r, u, v);
+        if (u == 0)
+            write_lse(r, l == 0.f ? -INFINITY : ref + ptx::lg2_approx(l));
+    }
+}
+#endif
+
+}  // namespace cache
+}  // namespace fa2

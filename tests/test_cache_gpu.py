@@ -190,6 +190,8 @@ def attend(c, G, Lq, kv_lens, q_lens=None, causal=True, window=None, workspace=T
     for _ in range(repeat):
         fa2().fa2_cache_attn(qd, *dev, i32(kv_lens), o, lse, causal=causal, q_lens=None if q_lens is None else i32(q_lens),
                              window=window, scale=scale, workspace=ws)
+    status, code = fa2().fa2_cache_get_device_error()
+    assert status == 0, f"device error {code:#x}"
     if ws is not None:   # left ready for the next call
         assert not ws[:1024].any()
     if check:
@@ -308,6 +310,18 @@ def test_long_context_is_shared_out_and_merged():
     again = attend(c, 8, 1, lens, q=q, check=False, repeat=5)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
     attend(c, 8, 1, lens, q=q, workspace=False)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunk_of_a_long_context(D):
+    """Blocks of rows cut over many CTAs and merged; the same bits each time, and without a workspace."""
+    lens = [2500, 700]
+    c = Cache(2, 1, D, 32, lens, seed=D + 4)
+    q = ref.bf16(c.rng.standard_normal((2, 2, 90, D)))
+    o, lse = attend(c, 2, 90, lens, [90, 71], q=q)
+    again = attend(c, 2, 90, lens, [90, 71], q=q, check=False, repeat=5)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    attend(c, 2, 90, lens, [90, 71], q=q, workspace=False)
 
 
 def test_many_sequences():
