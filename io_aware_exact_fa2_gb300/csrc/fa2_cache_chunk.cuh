@@ -462,18 +462,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                     // (-inf times a scale that underflowed to zero would be NaN, which fmaxf drops)
                     top = fmaxf(top, t * c[q] + static_cast<float>(ev[q]));
                 }
-                const bool raise = top > M + 8.f;
-                if (__any_sync(0xffffffffu, raise)) {
-                    float f = 1.f;
-                    if (raise) {
-                        f = ex2_approx(M - top);
-                        M = top;
-                        l *= f;
-                    }
-                    if (j > 0) {          // O in tensor memory stands for the old maximum
-                        if (!(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
-                            break;
-                        tc_fence_after();
+                const bool raise = top > M + 8.f, any = __any_sync(0xffffffffu, raise);
+                float f = 1.f;
+                if (raise) {
+                    f = ex2_approx(M - top);
+                    M = top;
+                    l *= f;
+                }
+                // A parity tells a phase from the one before only, so the wait below for the
+                // last tile's product needs this one taken for the last but one's, before
+                // the last can complete.
+                if (j > 0 && (any || j == n - 1)) {
+                    if (!(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
+                        break;
+                    tc_fence_after();
+                    if (any) {            // O in tensor memory stands for the old maximum
 #pragma unroll 1
                         for (int cc = 0; cc < D / 32; ++cc) {
                             uint32_t o[32];
@@ -519,9 +522,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
 
             // ---- O out of tensor memory: the unit's rows, or this part of them
             it += n;
-            // (a parity tells one phase from the next only: pass the last but one first)
-            if ((it >= 2 && !(ok = warp_wait(C::BAR_O_DONE, it & 1, CHUNK_ERR_SOFTMAX))) ||
-                !(ok = warp_wait(C::BAR_O_DONE, (it - 1) & 1, CHUNK_ERR_SOFTMAX)))
+            if (!(ok = warp_wait(C::BAR_O_DONE, (it - 1) & 1, CHUNK_ERR_SOFTMAX)))
                 break;
             tc_fence_after();
             const int first_cta = cut ? range.owner(line.at) : cta;
