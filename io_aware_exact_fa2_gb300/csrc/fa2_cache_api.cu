@@ -5,7 +5,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "fa2_cache.cuh"
+#include "fa2_cache_step.cuh"
 
 #define FA2_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -14,6 +14,21 @@ namespace cache {
 
 // Written by a kernel when one of its bounded waits runs out (first code wins).
 static __device__ int g_cache_error;
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
 
 namespace {
 

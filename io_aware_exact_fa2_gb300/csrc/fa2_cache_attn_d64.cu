@@ -1,28 +1,31 @@
 // fa2_cache_attn_d64.cu -- fa2_cache_attn for head dimension 64.
-#include "fa2_cache_attn.cuh"
 #include "fa2_cache_chunk.cuh"
+#include "fa2_cache_step.cuh"
 
 namespace fa2 {
 namespace cache {
 
 namespace {
-// Query rows of a key/value head up to which a step's kernel takes them.
-constexpr long long kFewRows = 32;
+// Query rows of a key/value head (Lq G): blocks of 8, 16 or 32 stream the cache with the
+// rows as columns of the products; more are rows themselves, 128 at a time.
+constexpr long long kFewRows = 64;
 
 template <class F>
 auto dispatch(long long rows, F f)
 {
-    if (rows <= 16)   // one matrix block; more share each key's conversion in two
-        return f(AttnCfg<64, 1>{});
+    if (rows <= 8)
+        return f(StepCfg<64, 8>{});
+    if (rows <= 16)
+        return f(StepCfg<64, 16>{});
     if (rows <= kFewRows)
-        return f(AttnCfg<64, 2>{});
+        return f(StepCfg<64, 32>{});
     return f(ChunkCfg<64>{});
 }
 
-template <int D, int MT>
-fa2_status launch(AttnCfg<D, MT>, const AttnArgs &a)
+template <int D, int R>
+fa2_status launch(StepCfg<D, R>, const AttnArgs &a)
 {
-    return launch_attn<AttnCfg<D, MT>>(a);
+    return launch_step<StepCfg<D, R>>(a);
 }
 template <int D>
 fa2_status launch(ChunkCfg<D>, const AttnArgs &a)

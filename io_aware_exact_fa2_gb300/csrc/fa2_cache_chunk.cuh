@@ -37,6 +37,7 @@ struct ChunkCfg {
     static constexpr int D = D_;
     static constexpr int R = 128;                    // query rows of a unit
     static constexpr int TILE = 64;                  // keys
+    static constexpr int ALIGN = CHUNK;              // where a unit's first tile may begin
     static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
     static constexpr int WARP_CONVERT = 4, WARP_MMA = 8;
     static constexpr int T = 32 * 12;                // (the last warpgroup: one issuing warp and three idle ones)
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
             int tile0, tile1;
             part_of(tile0, tile1);
             const int n = tile1 - tile0, b = line.b, h = line.h;
-            const int from = (line.span.lo & ~(CHUNK - 1)) + tile0 * TILE;
+            const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
             int all_lo, all_hi;
             line.seen_by_all(a, all_lo, all_hi);
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
             part_of(tile0, tile1);
             const int n = tile1 - tile0, b = line.b, h = line.h, rb = line.rb;
             const Seq s = line.s;
-            const int from = (line.span.lo & ~(CHUNK - 1)) + tile0 * TILE;
+            const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int rr = rb * R + row;
             const bool live = rr < s.n * a.G;
             const int tok = rr / a.G, hq = h * a.G + rr % a.G;

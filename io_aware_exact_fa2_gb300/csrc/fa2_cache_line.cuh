@@ -101,7 +101,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, const Seq &s, int rb)
         const long long lo = static_cast<long long>(s.kv) - s.n + i0 - a.window;
         p.lo = lo > 0 ? static_cast<int>(lo) : 0;
     }
-    const int from = p.lo & ~(CHUNK - 1);
+    const int from = p.lo & ~(C::ALIGN - 1);
     p.tiles = p.hi > from ? (p.hi - from + C::TILE - 1) / C::TILE : 0;
     p.tiles = p.tiles > 0 ? p.tiles : 1;   // a unit that sees nothing still writes its rows
     return p;

@@ -81,14 +81,17 @@ def gather(codes, scale, table_row, h, n):
 def attention(q, kc, vc, ks, vs, table, kv_lens, q_lens, causal, window, scale):
     """(o, lse, o_bound, lse_bound), float64 [B, Hq, Lq, D] and [B, Hq, Lq]; NaN bound: row not written.
 
-    The bounds, per row, from the kernel's arithmetic.  Products of codes and (scaled) bf16
-    are exact; a score sums D of them in fp32, each addition off by at most 2^-23 of the
-    partial sum (a bound for truncating adders too), so it is off by at most
-    ds = scale max_j sum_d |q_d k_jd| D 2^-23, plus 2^-21 (1 + |s|) for the
-    multiplication by the scale, the subtraction of the reference, the rounding of
-    log2 e and of 2^x.  Weights are rounded to fp16, 2^-11 of themselves (far down in the
-    type's range, where they are rounded by more, by at most 2^-31 of the largest each).
-    Sums over n keys add n 2^-22.  O is rounded to bf16: 2^-8 of itself.
+    The bounds, per row, from the kernels' arithmetic.  Products of codes and bf16 are
+    exact, whether q is one f16 or two e4m3 terms, except that a term of an element below
+    2^-14 of its row's largest is off by up to 2^-21 of that largest.  A score sums 2 D
+    products in fp32, each addition off by at most 2^-23 of the partial sum (a bound for
+    truncating adders too).  So a score is off by at most ds =
+    scale (max_j sum_d |q_d k_jd| 2 D 2^-23 + 2^-21 max|q| max_j sum_d |k_jd|), plus
+    2^-21 (1 + |s|) for the multiplication by the scale, the subtraction of the reference,
+    the rounding of log2 e and of 2^x.  Weights are rounded to fp16, 2^-11 of themselves,
+    or to three e4m3 terms, 2^-12 (far down in the types' ranges, where they are rounded
+    by more, by at most 2^-26 of the largest of 128 keys each).  Sums over n keys add
+    n 2^-22.  O is rounded to bf16: 2^-8 of itself.
     """
     B, Hq, Lq, D = q.shape
     H = kc.shape[1]
@@ -123,11 +126,15 @@ def attention(q, kc, vc, ks, vs, table, kv_lens, q_lens, causal, window, scale):
                         lse[b, h, i] = top + math.log(z)
                         o[b, h, i] = w @ vv
                         reach = scale * (np.abs(kk) @ np.abs(row)).max()
-                        ds = reach * D * 2.0 ** -23 + 2.0 ** -21 * (1 + np.abs(s).max())
+                        small_q = scale * 2.0 ** -21 * np.abs(row).max() * np.abs(kk).sum(1).max()
+                        ds = reach * 2 * D * 2.0 ** -23 + small_q + 2.0 ** -21 * (1 + np.abs(s).max())
                         lb[b, h, i] = ds + len(s) * 2.0 ** -23 + 2.0 ** -21 * (1 + abs(lse[b, h, i]))
                         rel = 2.0 ** -11 + 2 * ds + len(s) * 2.0 ** -22
                         mass = w @ np.abs(vv)
-                        small = 2.0 ** -31 * np.abs(vv).max() * len(s)
+                        # the weight of the largest of its 128 keys, for every key
+                        tile = np.zeros(-(-n // 128))
+                        np.maximum.at(tile, j[see] // 128, w)
+                        small = 2.0 ** -26 * (tile[j[see] // 128] @ np.ones_like(s)) * np.abs(vv).max()
                         ob[b, h, i] = 2.0 ** -8 * np.abs(o[b, h, i]) + (1 + 2.0 ** -8) * (rel * mass + small)
     return o, lse, ob, lb
 
