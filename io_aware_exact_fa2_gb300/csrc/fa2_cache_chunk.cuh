@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                                        static_cast<long long>(x / a.G) * a.o_sl;
                         *reinterpret_cast<uint2 *>(to + u * 4) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     };
-                    merge_parts<C>(parts, first_cta, last_cta, tid, 128, write_o, write_lse);
+                    const int live_rows = s.n * a.G - rb * R;
+                    merge_parts<C>(parts, first_cta, last_cta, live_rows < R ? live_rows : R, tid, 128, write_o, write_lse);
                 }
             }
             ++unit;

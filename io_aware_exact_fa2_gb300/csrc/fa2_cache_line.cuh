@@ -113,13 +113,21 @@ __device__ __forceinline__ int row_blocks(const AttnArgs &a, const Seq &s)
     return (s.n * a.G + C::R - 1) / C::R;
 }
 
+// x / y, both >= 0 and y > 0: 32-bit operands, the usual ones, divide several times faster.
+__device__ __forceinline__ long long divide(long long x, long long y)
+{
+    if (((x | y) >> 32) == 0)
+        return static_cast<unsigned>(x) / static_cast<unsigned>(y);
+    return x / y;
+}
+
 // One CTA's share of the line of tiles.
 struct Range {
     long long total;    // tiles of all units
     int grid;           // ranges
-    __device__ long long begin(int c) const { return total * c / grid; }
+    __device__ long long begin(int c) const { return divide(total * c, grid); }
     // the range that tile x lies in
-    __device__ int owner(long long x) const { return static_cast<int>(((x + 1) * grid + total - 1) / total - 1); }
+    __device__ int owner(long long x) const { return static_cast<int>(divide((x + 1) * grid + total - 1, total) - 1); }
 };
 
 // Tiles of one head's units of a sequence.
@@ -171,8 +179,8 @@ struct Line {
 };
 
 struct LineShared {
-    long long scan[32], off;
-    int b;
+    long long scan[32], off, per_head;
+    int b, kv, n;
 };
 
 // Lays out the line and finds this CTA's range of it, [first, end), and the unit it
@@ -187,9 +195,17 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     // the sequence
     const int per = (a.c.B + C::T - 1) / C::T;
     const int b0 = tid * per, b1 = b0 + per < a.c.B ? b0 + per : a.c.B;
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += tiles_of<C>(a, sequence(a, b)) * a.c.H;
+    long long mine = 0, mine_first = 0;
+    Seq seq_first{0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const Seq s = sequence(a, b);
+        const long long n = tiles_of<C>(a, s);
+        if (b == b0) {
+            seq_first = s;
+            mine_first = n;
+        }
+        mine += n * a.c.H;
+    }
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -219,23 +235,26 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     if (first >= end)
         return false;
     if (first >= before && first < before + mine) {
-        long long at = before;
+        long long at = before, n = mine_first;
         int b = b0;
-        for (;; ++b) {
-            const long long n = tiles_of<C>(a, sequence(a, b)) * a.c.H;
-            if (first < at + n)
-                break;
-            at += n;
+        Seq s = seq_first;
+        while (first >= at + n * a.c.H) {
+            at += n * a.c.H;
+            s = sequence(a, ++b);
+            n = tiles_of<C>(a, s);
         }
         sh.b = b;
         sh.off = at;
+        sh.per_head = n;
+        sh.kv = s.kv;
+        sh.n = s.n;
     }
     __syncthreads();
     line.b = sh.b;
     line.at = sh.off;
-    line.s = sequence(a, line.b);
-    const long long per_head = tiles_of<C>(a, line.s);
-    line.h = static_cast<int>((first - line.at) / per_head);
+    line.s = Seq{sh.kv, sh.n};
+    const long long per_head = sh.per_head;
+    line.h = static_cast<int>(divide(first - line.at, per_head));
     line.rb = 0;
     line.at += line.h * per_head;
     line.span = span_of<C>(a, line.s, 0);
@@ -249,14 +268,15 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
 
 // Merges the parts of a unit that ranges c0 .. c1 computed, always in that order, by
 // `threads` threads of which the caller is number `tid`; write(row, unit, value) takes
-// four values of O, write_lse(row, value) the log2-sum-exp2.
+// four values of O, write_lse(row, value) the log2-sum-exp2 of the first `rows` rows.
 template <class C, class W, class L>
-__device__ __forceinline__ void merge_parts(const Parts &parts, int c0, int c1, int tid, int threads, W write, L write_lse)
+__device__ __forceinline__ void merge_parts(const Parts &parts, int c0, int c1, int rows, int tid, int threads, W write,
+                                            L write_lse)
 {
     constexpr int R = C::R, D = C::D;
     const size_t slot_floats = Parts::slot_floats(R, D);
     auto slot = [&](int c) { return parts.data + (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * slot_floats; };
-    for (int i = tid; i < R * (D / 4); i += threads) {
+    for (int i = tid; i < rows * (D / 4); i += threads) {
         const int r = i / (D / 4), u = i % (D / 4);
         float top = -INFINITY;
         for (int c = c0; c <= c1; ++c)

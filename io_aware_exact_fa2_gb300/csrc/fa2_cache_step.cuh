@@ -62,8 +62,9 @@ struct StepCfg {
     // per row: the maxima of the four warps (two tiles), factors of the last two tiles, scale
     // factor, first and last visible key
     static constexpr int OFF_MAX = OFF_ROWS, OFF_FRAME = OFF_MAX + 2 * R * 16, OFF_SCALE = OFF_FRAME + 2 * R * 8;
-    static constexpr int OFF_LO = OFF_SCALE + R * 4, OFF_HI = OFF_LO + R * 4, OFF_L = OFF_HI + R * 4;
-    static constexpr int OFF_FLAGS = OFF_L + R * 16, OFF_NAN = OFF_FLAGS + 32, OFF_BAR = OFF_NAN + 16;
+    static constexpr int OFF_LO = OFF_SCALE + R * 4, OFF_HI = OFF_LO + R * 4, OFF_L = OFF_HI + R * 4;   // (OFF_L: four sums)
+    static constexpr int OFF_INV = OFF_L + R * 16, OFF_PLACE = OFF_INV + R * 8;   // 1 / sum and log2 of it; places in o and lse
+    static constexpr int OFF_FLAGS = OFF_PLACE + R * 16, OFF_NAN = OFF_FLAGS + 32, OFF_BAR = OFF_NAN + 16;
     static constexpr int NUM_BAR = 2 * SLOTS + 7;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // 1024: operand alignment
@@ -352,6 +353,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         float *const sh_scale = reinterpret_cast<float *>(smem + C::OFF_SCALE);       // [R]
         int *const sh_lo = reinterpret_cast<int *>(smem + C::OFF_LO), *const sh_hi = reinterpret_cast<int *>(smem + C::OFF_HI);
         float *const sh_l = reinterpret_cast<float *>(smem + C::OFF_L);               // [R][4]
+        float2 *const sh_inv = reinterpret_cast<float2 *>(smem + C::OFF_INV);         // [R]
+        longlong2 *const sh_place = reinterpret_cast<longlong2 *>(smem + C::OFF_PLACE);   // [R]; -1: not a row
         volatile uint32_t *const sh_flags = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAGS);   // [2][4]
         volatile uint32_t *const sh_nan = reinterpret_cast<uint32_t *>(smem + C::OFF_NAN);       // [4]
         auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };            // the four softmax warps
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             const Span span = line.span;
             const int from = (span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = span.hi < from + n * TILE ? span.hi : from + n * TILE;
-            const int rows = s.n * a.G;
+            const int rows = s.n * a.G, live = rows - rb * R;   // rows of the block (eight at a time below)
             int all_lo, all_hi;
             line.seen_by_all(a, all_lo, all_hi);
 
@@ -390,13 +393,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 constexpr int TPR = 128 / R, E = D / TPR;   // threads a row, elements a thread
                 const int r = tid / TPR, d0 = tid % TPR * E;
                 const int rr = rb * R + r, tok = rr / a.G, hq = h * a.G + rr % a.G;
-                const bool live = rr < rows;
+                const bool is_row = rr < rows;
                 const uint16_t *q = static_cast<const uint16_t *>(a.q) + b * a.q_sb + hq * a.q_sh + tok * a.q_sl + d0;
                 uint2 w[E / 4];
                 uint32_t top = 0;
 #pragma unroll
                 for (int k = 0; k < E / 4; ++k) {
-                    w[k] = live ? __ldg(reinterpret_cast<const uint2 *>(q) + k) : make_uint2(0, 0);
+                    w[k] = is_row ? __ldg(reinterpret_cast<const uint2 *>(q) + k) : make_uint2(0, 0);
                     const uint32_t m0 = max(w[k].x & 0x7fffu, w[k].x >> 16 & 0x7fffu), m1 = max(w[k].y & 0x7fffu, w[k].y >> 16 & 0x7fffu);
                     top = max(top, max(m0, m1));
                 }
@@ -424,8 +427,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const int pos = s.kv - s.n + tok;
                     const long long lo = static_cast<long long>(pos) - a.window;
                     sh_scale[r] = scale_log2 * pow2i(e);
-                    sh_hi[r] = !live ? 0 : a.causal ? pos + 1 : s.kv;
+                    sh_hi[r] = !is_row ? 0 : a.causal ? pos + 1 : s.kv;
                     sh_lo[r] = a.window >= 0 && lo > 0 ? static_cast<int>(lo) : 0;
+                    sh_place[r] = make_longlong2(is_row ? b * a.o_sb + hq * a.o_sh + tok * a.o_sl : -1,
+                                                 (static_cast<long long>(b) * a.Hq + hq) * a.Lq + tok);
                 }
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_Q_FULL);
@@ -448,24 +453,30 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 tc_fence_after();
                 const float2 *frame = sh_frame + ((g - 1) & 1) * R;
 #pragma unroll
-                for (int half = 0; half < C::HALVES; ++half) {
-                    uint32_t t0[R <= 8 ? 8 : R], t1[R <= 8 ? 8 : R], t2[R <= 8 ? 8 : R];
-                    const uint32_t addr = tmem + lanes + C::TM_O + half * C::NP;
-                    tmem_ld(addr, t0);
-                    tmem_ld(addr + R, t1);
-                    tmem_ld(addr + 2 * R, t2);
-                    tmem_wait_ld();
-                    tmem_pin(t0);
-                    tmem_pin(t1);
-                    tmem_pin(t2);
+                for (int r0 = 0; r0 < R; r0 += 8) {
+                    if (r0 >= live)
+                        break;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float2 f = frame[r];   // old frame -> new, tile -> new
-                        const float o = fmaf(__uint_as_float(t2[r]), 1.f / 256.f,
-                                             fmaf(__uint_as_float(t1[r]), 1.f / 16.f, __uint_as_float(t0[r])));
-                        acc[half][r] = fmaf(o, f.y, acc[half][r] * f.x);
-                        if (half == 0)
-                            l[r] = fmaf(psum[r], f.y, l[r] * f.x);
+                    for (int half = 0; half < C::HALVES; ++half) {
+                        uint32_t t0[8], t1[8], t2[8];
+                        const uint32_t addr = tmem + lanes + C::TM_O + half * C::NP + r0;
+                        tmem_ld(addr, t0);
+                        tmem_ld(addr + R, t1);
+                        tmem_ld(addr + 2 * R, t2);
+                        tmem_wait_ld();
+                        tmem_pin(t0);
+                        tmem_pin(t1);
+                        tmem_pin(t2);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = r0 + k;
+                            const float2 f = frame[r];   // old frame -> new, tile -> new
+                            const float o = fmaf(__uint_as_float(t2[k]), 1.f / 256.f,
+                                                 fmaf(__uint_as_float(t1[k]), 1.f / 16.f, __uint_as_float(t0[k])));
+                            acc[half][r] = fmaf(o, f.y, acc[half][r] * f.x);
+                            if (half == 0)
+                                l[r] = fmaf(psum[r], f.y, l[r] * f.x);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -486,63 +497,69 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 
                 warp_wait(C::BAR_S_FULL + par, g >> 1 & 1, STEP_ERR_SOFTMAX);
                 tc_fence_after();
-                float x[R];
-                {
-                    constexpr int N = R <= 8 ? 8 : R;
-                    uint32_t s0[N], s1[N];
-                    tmem_ld(tmem + lanes + C::TM_S + par * C::NQ, s0);
-                    tmem_ld(tmem + lanes + C::TM_S + par * C::NQ + R, s1);
+                float x[R];               // x + ev
+#pragma unroll
+                for (int r0 = 0; r0 < R; r0 += 8) {
+                    if (r0 >= live)
+                        break;
+                    uint32_t s0[8], s1[8];
+                    tmem_ld(tmem + lanes + C::TM_S + par * C::NQ + r0, s0);
+                    tmem_ld(tmem + lanes + C::TM_S + par * C::NQ + R + r0, s1);
                     tmem_wait_ld();
                     tmem_pin(s0);
                     tmem_pin(s1);
-                    tc_fence_before();
 #pragma unroll
-                    for (int r = 0; r < R; ++r)   // x + ev
-                        x[r] = fmaf(fmaf(__uint_as_float(s1[r]), 1.f / 16.f, __uint_as_float(s0[r])), sh_scale[r] * kf,
-                                    static_cast<float>(ev));
-                }
-                if (!whole)
+                    for (int k = 0; k < 8; ++k)
+                        x[r0 + k] = fmaf(fmaf(__uint_as_float(s1[k]), 1.f / 16.f, __uint_as_float(s0[k])), sh_scale[r0 + k] * kf,
+                                         static_cast<float>(ev));
+                    if (!whole)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        x[r] = there && pos >= sh_lo[r] && pos < sh_hi[r] ? x[r] : -INFINITY;
-                // the rows' maxima over the tile
-                {
+                        for (int k = 0; k < 8; ++k)
+                            x[r0 + k] = there && pos >= sh_lo[r0 + k] && pos < sh_hi[r0 + k] ? x[r0 + k] : -INFINITY;
+                    // the rows' maxima over the warp's keys
                     float mine = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float m = warp_max(x[r]);
-                        mine = lane == r ? m : mine;
+                    for (int k = 0; k < 8; ++k) {
+                        const float m = warp_max(x[r0 + k]);
+                        mine = lane == k ? m : mine;
                     }
-                    if (lane < R)
-                        sh_max[(par * R + lane) * 4 + warp] = mine;
+                    if (lane < 8)
+                        sh_max[(par * R + r0 + lane) * 4 + warp] = mine;
+                }
+                tc_fence_before();
+                {
                     const bool some = __any_sync(0xffffffffu, !whole);
                     if (lane == 0)
                         sh_flags[par * 4 + warp] = some;
                 }
                 sync();
+                // the tile's references, above the maxima; a row's frame is moved by its own thread
+                auto reference = [&](int r) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(sh_max + (par * R + r) * 4);
+                    return fmaxf(ceilf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))), static_cast<float>(NONE));
+                };
+                if (tid < R && tid < live) {
+                    const int mt = static_cast<int>(reference(tid)), now = mt > M ? mt : M;
+                    sh_frame[par * R + tid] = make_float2(pow2i(M - now), pow2i(mt - now));
+                    M = now;
+                }
                 // weights
                 uint32_t p[3][R / 2];
                 float psum_new[R];
                 const float lf = pow2i(-ev);
 #pragma unroll
-                for (int r = 0; r < R; r += 2) {
-                    float y[2];
+                for (int r0 = 0; r0 < R; r0 += 8) {
+                    if (r0 >= live)
+                        break;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 m4 = *reinterpret_cast<const float4 *>(sh_max + (par * R + r + k) * 4);
-                        const float top = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                        const float m = fminf(fmaxf(ceilf(top), static_cast<float>(NONE)), static_cast<float>(-NONE));
-                        y[k] = ex2_approx(x[r + k] - m + 8.f);
-                        psum_new[r + k] = y[k] * lf;
-                        if (tid == r + k) {   // this row's frame
-                            const int mt = static_cast<int>(m), now = mt > M ? mt : M;
-                            sh_frame[par * R + r + k] = make_float2(pow2i(M - now), pow2i(mt - now));
-                            M = now;
-                        }
+                    for (int r = r0; r < r0 + 8; r += 2) {
+                        float y0 = ex2_approx(x[r] - reference(r) + 8.f), y1 = ex2_approx(x[r + 1] - reference(r + 1) + 8.f);
+                        psum_new[r] = y0 * lf;
+                        psum_new[r + 1] = y1 * lf;
+#pragma unroll
+                        for (int term = 0; term < 3; ++term)
+                            p[term][r / 2] = take_term(y0, y1);
                     }
-#pragma unroll
-                    for (int term = 0; term < 3; ++term)
-                        p[term][r / 2] = take_term(y[0], y[1]);
                 }
                 // Keys that not every row sees: what lies in their slots' place in shared memory
                 // may be anything, and NaN times a weight of 0 is NaN.
@@ -596,16 +613,20 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 if (j > 0)
                     add_tile(g);   // (and its product no longer reads the weights' place)
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    psum[r] = psum_new[r];
+                for (int r0 = 0; r0 < R; r0 += 8) {
+                    if (r0 >= live)
+                        break;
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
+                    for (int r = r0; r < r0 + 8; ++r) {
+                        psum[r] = psum_new[r];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int row = term * R + r;
-                        smem[C::OFF_P + row * 128 + (((tid >> 4) ^ (row & 7)) << 4) + (tid & 15)] =
-                            static_cast<uint8_t>(p[term][r / 2] >> (r & 1) * 8);
+                        for (int term = 0; term < 3; ++term) {
+                            const int row = term * R + r;
+                            smem[C::OFF_P + row * 128 + (((tid >> 4) ^ (row & 7)) << 4) + (tid & 15)] =
+                                static_cast<uint8_t>(p[term][r / 2] >> (r & 1) * 8);
+                        }
                     }
+                }
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_P_FULL);
             }
@@ -615,53 +636,62 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 
             // ---- O and LSE of the unit's rows, or of this part of them
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float v = l[r];
+            for (int r0 = 0; r0 < R; r0 += 8) {
+                if (r0 >= live)
+                    break;
+                float mine = 0.f;
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    v += __shfl_xor_sync(0xffffffffu, v, d);
-                l[r] = v;
+                for (int k = 0; k < 8; ++k) {
+                    float v = l[r0 + k];
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1)
+                        v += __shfl_xor_sync(0xffffffffu, v, d);
+                    mine = lane == k ? v : mine;
+                }
+                if (lane < 8)
+                    sh_l[(r0 + lane) * 4 + warp] = mine;
             }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (lane == r)
-                    sh_l[r * 4 + warp] = l[r];
             sync();
+            if (tid < R) {
+                const float4 l4 = *reinterpret_cast<const float4 *>(sh_l + tid * 4);
+                const float sum = tid < live ? (l4.x + l4.y) + (l4.z + l4.w) : 0.f;
+                sh_inv[tid] = sum == 0.f ? make_float2(0.f, -INFINITY)
+                                         : make_float2(1.f / sum, static_cast<float>(M) - 8.f + lg2_approx(sum));
+            }
             const int first_cta = cut ? range.owner(line.at) : cta;
             const int last_cta = cut ? range.owner(line.at + span.tiles - 1) : cta;
             const bool alone = first_cta == last_cta;
             float *const part =
                 cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
-            auto row_of = [&](int r) {   // row r's place in o
-                const int x = rb * R + r;
-                return static_cast<uint16_t *>(a.o) + b * a.o_sb + (h * a.G + x % a.G) * a.o_sh +
-                       static_cast<long long>(x / a.G) * a.o_sl;
-            };
+            uint16_t *const o = static_cast<uint16_t *>(a.o);
             auto write_lse = [&](int r, float v) {
-                const int x = rb * R + r;
-                if (x < rows)
-                    a.lse[(static_cast<long long>(b) * a.Hq + h * a.G + x % a.G) * a.Lq + x / a.G] = v * 0.69314718055994531f;
+                if (r < live)
+                    a.lse[sh_place[r].y] = v * 0.69314718055994531f;
             };
+            sync();
+            if (tid < R) {
+                if (alone)
+                    write_lse(tid, sh_inv[tid].y);
+                else
+                    part[R * D + tid] = sh_inv[tid].y;
+            }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float4 l4 = *reinterpret_cast<const float4 *>(sh_l + r * 4);
-                const float sum = (l4.x + l4.y) + (l4.z + l4.w);
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                if (tid == r) {
-                    const float lse2 = sum == 0.f ? -INFINITY : static_cast<float>(M) - 8.f + lg2_approx(sum);
-                    if (alone)
-                        write_lse(r, lse2);
-                    else
-                        part[R * D + r] = lse2;
-                }
+            for (int r0 = 0; r0 < R; r0 += 8) {
 #pragma unroll
-                for (int half = 0; half < C::HALVES; ++half) {
-                    const float v = nan_rows[half] >> r & 1 ? __uint_as_float(0x7fc00000u) : acc[half][r] * inv;
-                    const int d = half * 128 + tid;
-                    if (alone && rb * R + r < rows && owns_d)
-                        row_of(r)[d] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-                    else if (!alone && owns_d)
-                        part[r * D + d] = v;
+                for (int k = 0; k < 8; ++k) {
+                    const int r = r0 + k;
+                    if (r >= live || !owns_d)
+                        break;
+                    const float inv = sh_inv[r].x;
+#pragma unroll
+                    for (int half = 0; half < C::HALVES; ++half) {
+                        const float v = nan_rows[half] >> r & 1 ? __uint_as_float(0x7fc00000u) : acc[half][r] * inv;
+                        const int d = half * 128 + tid;
+                        if (alone)
+                            o[sh_place[r].x + d] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+                        else
+                            part[r * D + d] = v;
+                    }
                 }
             }
             if (!alone) {
@@ -678,13 +708,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 if (*last) {
                     __threadfence();
                     auto write_o = [&](int r, int u, const float4 &v) {
-                        if (rb * R + r < rows)
-                            *reinterpret_cast<uint2 *>(row_of(r) + u * 4) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                        if (r < live)
+                            *reinterpret_cast<uint2 *>(o + sh_place[r].x + u * 4) =
+                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     };
-                    merge_parts<C>(parts, first_cta, last_cta, tid, 128, write_o, write_lse);
+                    merge_parts<C>(parts, first_cta, last_cta, live < R ? live : R, tid, 128, write_o, write_lse);
                 }
             }
             ++unit;
+            sync();   // the rows' places are free again
         } while (next_unit());
     }
 
