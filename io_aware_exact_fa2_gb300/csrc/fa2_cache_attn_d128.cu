@@ -6,8 +6,8 @@ namespace fa2 {
 namespace cache {
 
 namespace {
-// Query rows of a key/value head (Lq G): blocks of 8, 16 or 32 stream the cache with the
-// rows as columns of the products; more are rows themselves, 128 at a time.
+// Query rows of a key/value head (Lq G): blocks of 8 or 16 stream the cache with the rows
+// as columns of the products; more are rows themselves, 128 at a time.
 constexpr long long kFewRows = 64;
 
 template <class F>
@@ -15,10 +15,8 @@ auto dispatch(long long rows, F f)
 {
     if (rows <= 8)
         return f(StepCfg<128, 8>{});
-    if (rows <= 16)
-        return f(StepCfg<128, 16>{});
     if (rows <= kFewRows)
-        return f(StepCfg<128, 32>{});
+        return f(StepCfg<128, 16>{});
     return f(ChunkCfg<128>{});
 }
 

@@ -92,7 +92,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, const Seq &s, int rb)
 {
     const int rows = s.n * a.G;
     const int r1 = (rb + 1) * C::R < rows ? (rb + 1) * C::R : rows;
-    const int i0 = rb * C::R / a.G, i1 = (r1 - 1) / a.G;
+    const int i0 = rb ? rb * C::R / a.G : 0, i1 = r1 == rows ? s.n - 1 : (r1 - 1) / a.G;
     Span p;
     p.hi = a.causal ? s.kv - s.n + i1 + 1 : s.kv;
     p.hi = p.hi < 0 ? 0 : p.hi;
@@ -171,7 +171,7 @@ struct Line {
     {
         const int rows = s.n * a.G;
         const int r1 = (rb + 1) * C::R < rows ? (rb + 1) * C::R : rows;
-        const int i0 = rb * C::R / a.G, i1 = (r1 - 1) / a.G;
+        const int i0 = rb ? rb * C::R / a.G : 0, i1 = r1 == rows ? s.n - 1 : (r1 - 1) / a.G;
         hi = a.causal ? s.kv - s.n + i0 + 1 : s.kv;
         const long long from = static_cast<long long>(s.kv) - s.n + i1 - a.window;
         lo = a.window >= 0 && from > 0 ? static_cast<int>(from) : 0;

@@ -8,10 +8,10 @@
 // Mathematics.  The tensor cores take the cache's codes as they are (kind::f8f6f4); what
 // multiplies them is split into e4m3 terms:
 //     q 2^-e = q0 + 2^-4 q1             (e: largest magnitude of the row in [128, 256))
-// is exact for a bf16 q but where an element is below 2^-14 of its row's largest (then off
-// by at most 2^-21 of that), because e4m3 holds half of bf16's eight bits; and
-//     p = p0 + 2^-4 p1 + 2^-8 p2        (p in [0, 256])
-// is off by at most 2^-12 of p, and 2^-26 of the tile's largest.  Both products are taken
+// is exact for a bf16 q, because e4m3 holds half of bf16's eight bits (an element below
+// 2^-14 of its row's largest is off by at most 2^-21 of that); and
+//     p = p0 + 2^-4 p1 + 2^-8 p2        (p in [0, 256], first rounded to f16)
+// is off by at most 2^-11 of p, or 2^-26 of the tile's largest.  Both products are taken
 // transposed, so that the cache is the 128-row operand and the few query rows are columns:
 //     S^T [128 keys, 2 R]  = K  [q0 | q1]^T
 //     O^T [D, 3 R]         = V^T [p0 | p1 | p2]^T
@@ -47,7 +47,7 @@ struct StepCfg {
     static constexpr int R = R_;                     // query rows of a unit
     static constexpr int TILE = 128;                 // keys
     static constexpr int ALIGN = 128;                // whole pages: a tile begins at a multiple
-    static constexpr int CTAS = D == 64 ? (R <= 16 ? 3 : 2) : D == 128 ? 2 : 1;   // an SM
+    static constexpr int CTAS = D == 64 ? (R == 8 ? 3 : 2) : D == 128 ? 2 : 1;   // an SM
     static constexpr int WARP_LOAD = 4, WARP_MMA = 5;
     static constexpr int T = 32 * 6;
 
@@ -55,7 +55,7 @@ struct StepCfg {
     static constexpr int PANELS = D / ROW;
     static constexpr int PANEL = TILE * ROW;         // of a slot
     static constexpr int SLOT = TILE * D;            // keys or values of a tile
-    static constexpr int SLOTS = D == 64 ? 6 : D == 128 ? (R <= 16 ? 6 : 5) : 5;
+    static constexpr int SLOTS = D == 256 ? 5 : 6;
     static constexpr int NQ = 2 * R, Q_PANEL = NQ * ROW;            // rows [q0 | q1]
     static constexpr int NP = (3 * R + 15) / 16 * 16;               // rows [p0 | p1 | p2], 128 bytes each
     static constexpr int OFF_RING = 0, OFF_P = SLOTS * SLOT, OFF_Q = OFF_P + NP * 128, OFF_ROWS = OFF_Q + NQ * D;
@@ -64,7 +64,8 @@ struct StepCfg {
     static constexpr int OFF_MAX = OFF_ROWS, OFF_FRAME = OFF_MAX + 2 * R * 16, OFF_SCALE = OFF_FRAME + 2 * R * 8;
     static constexpr int OFF_LO = OFF_SCALE + R * 4, OFF_HI = OFF_LO + R * 4, OFF_L = OFF_HI + R * 4;   // (OFF_L: four sums)
     static constexpr int OFF_INV = OFF_L + R * 16, OFF_PLACE = OFF_INV + R * 8;   // 1 / sum and log2 of it; places in o and lse
-    static constexpr int OFF_FLAGS = OFF_PLACE + R * 16, OFF_NAN = OFF_FLAGS + 32, OFF_BAR = OFF_NAN + 16;
+    static constexpr int OFF_FLAGS = OFF_PLACE + R * 16, OFF_NAN = OFF_FLAGS + 32, OFF_INFO = OFF_NAN + 16;
+    static constexpr int INFO_BYTES = TILE / CHUNK * 4, OFF_BAR = OFF_INFO + 4 * INFO_BYTES;   // (ring of four tiles)
     static constexpr int NUM_BAR = 2 * SLOTS + 7;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // 1024: operand alignment
@@ -76,10 +77,14 @@ struct StepCfg {
     static constexpr int BAR_FULL = 0, BAR_EMPTY = SLOTS, BAR_Q_FULL = 2 * SLOTS, BAR_Q_EMPTY = BAR_Q_FULL + 1,
                          BAR_S_FULL = BAR_Q_FULL + 2, BAR_P_FULL = BAR_Q_FULL + 4, BAR_O_DONE = BAR_Q_FULL + 5,
                          BAR_DRAIN = BAR_Q_FULL + 6;
-    static_assert(R % 8 == 0 && R <= 32 && TM_USED <= 512 && CTAS * TMEM_COLS <= 512, "tensor memory holds CTAS of them");
+    static_assert(SLOTS <= 6, "the ring of four tiles' scales");
+    static_assert(R % 8 == 0 && R <= 16 && TM_USED <= 512 && CTAS * TMEM_COLS <= 512, "tensor memory holds CTAS of them");
     static_assert(CTAS * (SMEM_BYTES + 1024 + 512) <= 228 * 1024, "an SM holds CTAS of them");
     static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && Q_PANEL % 512 == 0, "swizzle atoms");
 };
+
+// A page's scales as the loading warp hands them on: key byte, value byte, this bit (0: no page).
+constexpr uint32_t STEP_PAGE = 1u << 16;
 
 // Error codes of waits that ran out (bits 8-11 the waiting role).
 constexpr int STEP_ERR_SOFTMAX = 12 << 8, STEP_ERR_LOAD = 13 << 8, STEP_ERR_MMA = 14 << 8, STEP_ERR_DRAIN = 15 << 8;
@@ -150,23 +155,21 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uin
            static_cast<uint64_t>(sbo >> 4 & 0x3FFFu) << 32 | 1ull << 46 | 4ull << 61;
 }
 
-// Two fp32 -> two e4m3 codes (round to nearest even, saturating), `lo` in bits [0,8).
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
+// Takes the next e4m3 term off an f16 pair: its codes (round to nearest even, saturating),
+// and 16 times what is left, exactly: the rounding error of four bits' worth of eleven.
+__device__ __forceinline__ uint32_t take_term(uint32_t &pair)
 {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Takes the next e4m3 term off two values: its codes, and 16 times what is left.
-__device__ __forceinline__ uint32_t take_term(float &a, float &b)
-{
-    const uint32_t w = pack_e4m3x2(a, b);
-    float x, y;
-    unpack_f16x2(e4m3x2_to_f16x2(w), x, y);
-    a = (a - x) * 16.f;
-    b = (b - y) * 16.f;
-    return w;
+    uint32_t codes, rest;
+    asm("{\n\t.reg .b16 c;\n\t.reg .b32 x;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 c, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 x, c;\n\t"
+        "sub.rn.f16x2 x, %2, x;\n\t"
+        "mul.rn.f16x2 %1, x, %3;\n\t"
+        "cvt.u32.u16 %0, c;\n\t}"
+        : "=r"(codes), "=r"(rest)
+        : "r"(pair), "r"(0x4c004c00u));   // 16, 16
+    pair = rest;
+    return codes;
 }
 
 template <class C>
@@ -223,6 +226,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         tile1 = cut && end < line.at + line.span.tiles ? static_cast<int>(end - line.at) : line.span.tiles;
     };
     auto next_unit = [&]() { return line.next(a) && line.at < end; };
+    uint32_t *const sh_info = reinterpret_cast<uint32_t *>(smem + C::OFF_INFO);   // [4][8 groups of 16 keys]
     // tile g's keys are item 2 g of the ring, its values item 2 g + 1
     uint32_t it = 0, unit = 0;   // tiles and units before the present unit
 
@@ -242,13 +246,22 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             const int n = tile1 - tile0, h = line.h;
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
-            auto page_at = [&](int j) {
-                const long long pos = from + static_cast<long long>(j) * TILE + (static_cast<long long>(lane) << a.c.page_shift);
-                const bool seen = lane < pages && pos < stop && pos + (1ll << a.c.page_shift) > line.span.lo;
-                return seen ? page_of(a.c, line.b, static_cast<int>(pos >> a.c.page_shift)) : -1;
+            auto page_at = [&](int j) {                    // -1: none, or not seen
+                const int pos = from + j * TILE + (lane << a.c.page_shift);
+                const bool seen = j < n && lane < pages && pos < stop && pos + (1 << a.c.page_shift) > line.span.lo;
+                return seen ? page_of(a.c, line.b, pos >> a.c.page_shift) : -1;
             };
-            int id = page_at(0), id_next = page_at(1);
+            auto scales_of = [&](int page) -> uint32_t {
+                if (page < 0)
+                    return 0;
+                const long long i = static_cast<long long>(page) * a.c.H + h;
+                return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | STEP_PAGE;
+            };
+            int id = page_at(0), id_next = page_at(1);     // pages two tiles ahead, scales one
+            uint32_t sc = scales_of(id);
             for (int j = 0; j < n && ok; ++j) {
+                const int id_after = page_at(j + 2);
+                const uint32_t sc_next = scales_of(id_next);
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * page_bytes;
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
@@ -257,6 +270,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         warp_wait(C::BAR_EMPTY + slot, (item / SLOTS - 1) & 1, STEP_ERR_LOAD);
                     if (!ok)
                         break;
+                    // (the tile four back has been through its softmax: its values' slot came
+                    // back before the last tile was loaded)
+                    if (side == 0 && lane < pages)
+                        for (int k = 0; k < 1 << (a.c.page_shift - 4); ++k)
+                            sh_info[((it + j) & 3) * (TILE / CHUNK) + (lane << (a.c.page_shift - 4)) + k] = sc;
+                    __syncwarp();
                     if (lane == 0)
                         mbar_arrive_expect_tx(bar(C::BAR_FULL + slot), bytes);
                     __syncwarp();
@@ -268,7 +287,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     issued = item + 1;
                 }
                 id = id_next;
-                id_next = page_at(j + 2);
+                id_next = id_after;
+                sc = sc_next;
             }
             it += n;
         } while (ok && next_unit());
@@ -373,19 +393,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             int all_lo, all_hi;
             line.seen_by_all(a, all_lo, all_hi);
 
-            // this thread's key: page (two tiles ahead) and scales (one)
-            auto page_at = [&](int j) {
-                const long long pos = from + static_cast<long long>(j) * TILE + tid;
-                return pos >= span.lo && pos < stop ? page_of(a.c, b, static_cast<int>(pos) >> a.c.page_shift) : -1;
-            };
-            auto scales_of = [&](int id) -> uint32_t {
-                if (id < 0)
-                    return 0;
-                const long long i = static_cast<long long>(id) * a.c.H + h;
-                return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | 1u << 16;
-            };
-            int id_next = page_at(0), id_after = page_at(1);
-
             // ---- Q as two e4m3 terms; TPR threads a row
             if (unit > 0)
                 warp_wait(C::BAR_Q_EMPTY, (unit - 1) & 1, STEP_ERR_SOFTMAX);
@@ -412,12 +419,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
 #pragma unroll
                 for (int k = 0; k < E / 4; ++k) {
-                    float x0 = __uint_as_float(w[k].x << 16) * f, x1 = __uint_as_float(w[k].x & 0xffff0000u) * f;
-                    float x2 = __uint_as_float(w[k].y << 16) * f, x3 = __uint_as_float(w[k].y & 0xffff0000u) * f;
+                    uint32_t x01 = pack_f16x2(__uint_as_float(w[k].x << 16) * f, __uint_as_float(w[k].x & 0xffff0000u) * f);
+                    uint32_t x23 = pack_f16x2(__uint_as_float(w[k].y << 16) * f, __uint_as_float(w[k].y & 0xffff0000u) * f);
                     const int d = d0 + 4 * k, panel = d / C::ROW, col = d % C::ROW;
 #pragma unroll
                     for (int term = 0; term < 2; ++term) {
-                        const uint32_t lo = take_term(x0, x1), hi = take_term(x2, x3);
+                        const uint32_t lo = take_term(x01), hi = take_term(x23);
                         const int row = term * R + r, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
                         *reinterpret_cast<uint32_t *>(smem + C::OFF_Q + panel * C::Q_PANEL + row * C::ROW +
                                                       (((col >> 4) ^ x) << 4) + (col & 15)) = lo | hi << 16;
@@ -435,7 +442,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_Q_FULL);
             }
-            uint32_t sc_next = scales_of(id_next);
             sync();   // the rows' scales and limits are there
 
             float acc[C::HALVES][R], l[R], psum[R];
@@ -485,18 +491,14 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = it + j, par = g & 1;
                 const int pos = from + j * TILE + tid;
-                const uint32_t sc = sc_next;
-                id_next = id_after;
-                sc_next = scales_of(id_next);
-                id_after = page_at(j + 2);
+                warp_wait(C::BAR_S_FULL + par, g >> 1 & 1, STEP_ERR_SOFTMAX);
+                tc_fence_after();
+                const uint32_t sc = sh_info[(g & 3) * (TILE / CHUNK) + (tid >> 4)];
                 const int ek = static_cast<int>(sc & 255) - 127;
-                const bool there = sc != 0, nan_scale = there && (sc >> 8 & 255) == 255;
+                const bool there = sc != 0 && pos >= span.lo && pos < stop, nan_scale = there && (sc >> 8 & 255) == 255;
                 const int ev = there && !nan_scale ? static_cast<int>(sc >> 8 & 255) - 127 : 0;
                 const float kf = ek == 128 ? __uint_as_float(0x7fc00000u) : pow2i(ek);
                 const bool whole = there && !nan_scale && pos >= all_lo && pos < all_hi;   // every row sees the key
-
-                warp_wait(C::BAR_S_FULL + par, g >> 1 & 1, STEP_ERR_SOFTMAX);
-                tc_fence_after();
                 float x[R];               // x + ev
 #pragma unroll
                 for (int r0 = 0; r0 < R; r0 += 8) {
@@ -553,12 +555,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         break;
 #pragma unroll
                     for (int r = r0; r < r0 + 8; r += 2) {
-                        float y0 = ex2_approx(x[r] - reference(r) + 8.f), y1 = ex2_approx(x[r + 1] - reference(r + 1) + 8.f);
+                        const float y0 = ex2_approx(x[r] - reference(r) + 8.f), y1 = ex2_approx(x[r + 1] - reference(r + 1) + 8.f);
                         psum_new[r] = y0 * lf;
                         psum_new[r + 1] = y1 * lf;
+                        uint32_t y = pack_f16x2(y0, y1);
 #pragma unroll
                         for (int term = 0; term < 3; ++term)
-                            p[term][r / 2] = take_term(y0, y1);
+                            p[term][r / 2] = take_term(y);
                     }
                 }
                 // Keys that not every row sees: what lies in their slots' place in shared memory
