@@ -37,6 +37,7 @@ struct ChunkCfg {
     static constexpr int D = D_;
     static constexpr int R = 128;                    // query rows of a unit
     static constexpr int TILE = 64;                  // keys
+    static constexpr int UNIT_COST = 4, MIN_TILES = 4;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = CHUNK;              // where a unit's first tile may begin
     static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
     static constexpr int WARP_CONVERT = 4, WARP_MMA = 8;

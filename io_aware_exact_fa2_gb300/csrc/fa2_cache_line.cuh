@@ -4,6 +4,8 @@
 // A unit is a block of C::R query rows of one (sequence, key/value head); it spans the
 // tiles of C::TILE keys that any of its rows sees.  Units lie on the line in the order
 // sequence, head, row block, so that CTAs that run side by side read the same keys.
+// A unit is C::UNIT_COST tiles longer on the line than it is, for what it costs to begin and
+// end one; a range that holds only of those has nothing to do with the unit.
 // Lengths are device data, so every CTA lays out the line for itself.
 #pragma once
 
@@ -14,8 +16,6 @@ namespace fa2 {
 namespace cache {
 
 constexpr int CHUNK = 16;                 // keys of the smallest piece; divides every page size
-constexpr int MIN_TILES = 4;              // least tiles a CTA's range is cut down to
-
 // Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
 // R rows: O [R, D] fp32, then the log2-sum-exp2 [R].
 struct Parts {
@@ -57,7 +57,7 @@ int line_grid(const AttnArgs &a, bool cut)
     const long long most = a.num_sms * C::CTAS;
     const long long blocks = (static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R;
     const long long tiles = ((static_cast<long long>(a.c.max_pages) << a.c.page_shift) + C::TILE - 1) / C::TILE + 1;
-    long long grid = cut ? (tiles + MIN_TILES - 1) / MIN_TILES : 1;
+    long long grid = cut ? (tiles + C::UNIT_COST + C::MIN_TILES - 1) / C::MIN_TILES : 1;
     grid = grid > most ? most : grid;
     grid *= blocks > most ? most : blocks;
     grid = grid > most ? most : grid;
@@ -123,21 +123,21 @@ __device__ __forceinline__ long long divide(long long x, long long y)
 
 // One CTA's share of the line of tiles.
 struct Range {
-    long long total;    // tiles of all units
+    long long total;    // the line's length
     int grid;           // ranges
     __device__ long long begin(int c) const { return divide(total * c, grid); }
     // the range that tile x lies in
     __device__ int owner(long long x) const { return static_cast<int>(divide((x + 1) * grid + total - 1, total) - 1); }
 };
 
-// Tiles of one head's units of a sequence.
+// Length on the line of one head's units of a sequence.
 template <class C>
 __device__ __forceinline__ long long tiles_of(const AttnArgs &a, const Seq &s)
 {
     long long n = 0;
     const int blocks = row_blocks<C>(a, s);
     for (int rb = 0; rb < blocks; ++rb)
-        n += span_of<C>(a, s, rb).tiles;
+        n += span_of<C>(a, s, rb).tiles + C::UNIT_COST;
     return n;
 }
 
@@ -151,7 +151,7 @@ struct Line {
 
     __device__ __forceinline__ bool next(const AttnArgs &a)   // the following unit; false at the line's end
     {
-        at += span.tiles;
+        at += span.tiles + C::UNIT_COST;
         if (++rb == row_blocks<C>(a, s)) {
             rb = 0;
             if (++h == a.c.H) {
@@ -225,7 +225,7 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     if (total == 0)
         return false;
     range.total = total;
-    const long long most = cut ? (total + MIN_TILES - 1) / MIN_TILES : total;
+    const long long most = cut ? divide(total + C::MIN_TILES - 1, C::MIN_TILES) : total;
     range.grid = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
     const int cta = blockIdx.x;
     if (cta >= range.grid)
@@ -258,7 +258,7 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     line.rb = 0;
     line.at += line.h * per_head;
     line.span = span_of<C>(a, line.s, 0);
-    while (line.at + line.span.tiles <= first)
+    while (line.at + line.span.tiles <= first)   // (next() may end past `first`, in a unit's extra length)
         if (!line.next(a))
             return false;
     if (!cut && line.at < first && !line.next(a))

@@ -46,6 +46,7 @@ struct StepCfg {
     static constexpr int D = D_;
     static constexpr int R = R_;                     // query rows of a unit
     static constexpr int TILE = 128;                 // keys
+    static constexpr int UNIT_COST = 2, MIN_TILES = 2;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = 128;                // whole pages: a tile begins at a multiple
     static constexpr int CTAS = D == 64 ? (R == 8 ? 3 : 2) : D == 128 ? 2 : 1;   // an SM
     static constexpr int WARP_LOAD = 4, WARP_MMA = 5;
@@ -113,21 +114,11 @@ inline bool page_map(EncodeTiled encode, CUtensorMap *m, const Half &x, const Vi
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
 {
-    static_assert(N == 8 || N == 16 || N == 32, "");
-    if constexpr (N == 32)
-        ptx::tmem_ld32(taddr, r);
-    else if constexpr (N == 16)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-                     "%15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(taddr)
-                     : "memory");
-    else
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr)
-                     : "memory");
+    static_assert(N == 4, "");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Keeps uses of loaded registers below the wait.
@@ -389,7 +380,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             const Span span = line.span;
             const int from = (span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = span.hi < from + n * TILE ? span.hi : from + n * TILE;
-            const int rows = s.n * a.G, live = rows - rb * R;   // rows of the block (eight at a time below)
+            const int rows = s.n * a.G, live = rows - rb * R;   // rows of the block (four at a time below)
             int all_lo, all_hi;
             line.seen_by_all(a, all_lo, all_hi);
 
@@ -442,6 +433,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_Q_FULL);
             }
+            const int first_cta = cut ? range.owner(line.at) : cta;
+            const int last_cta = cut ? range.owner(line.at + span.tiles - 1) : cta;
+            const bool alone = first_cta == last_cta;
+            float *const part =
+                cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
             sync();   // the rows' scales and limits are there
 
             float acc[C::HALVES][R], l[R], psum[R];
@@ -459,12 +455,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 tc_fence_after();
                 const float2 *frame = sh_frame + ((g - 1) & 1) * R;
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 8) {
+                for (int r0 = 0; r0 < R; r0 += 4) {
                     if (r0 >= live)
                         break;
 #pragma unroll
                     for (int half = 0; half < C::HALVES; ++half) {
-                        uint32_t t0[8], t1[8], t2[8];
+                        uint32_t t0[4], t1[4], t2[4];
                         const uint32_t addr = tmem + lanes + C::TM_O + half * C::NP + r0;
                         tmem_ld(addr, t0);
                         tmem_ld(addr + R, t1);
@@ -474,7 +470,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         tmem_pin(t1);
                         tmem_pin(t2);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < 4; ++k) {
                             const int r = r0 + k;
                             const float2 f = frame[r];   // old frame -> new, tile -> new
                             const float o = fmaf(__uint_as_float(t2[k]), 1.f / 256.f,
@@ -501,31 +497,31 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const bool whole = there && !nan_scale && pos >= all_lo && pos < all_hi;   // every row sees the key
                 float x[R];               // x + ev
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 8) {
+                for (int r0 = 0; r0 < R; r0 += 4) {
                     if (r0 >= live)
                         break;
-                    uint32_t s0[8], s1[8];
+                    uint32_t s0[4], s1[4];
                     tmem_ld(tmem + lanes + C::TM_S + par * C::NQ + r0, s0);
                     tmem_ld(tmem + lanes + C::TM_S + par * C::NQ + R + r0, s1);
                     tmem_wait_ld();
                     tmem_pin(s0);
                     tmem_pin(s1);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = 0; k < 4; ++k)
                         x[r0 + k] = fmaf(fmaf(__uint_as_float(s1[k]), 1.f / 16.f, __uint_as_float(s0[k])), sh_scale[r0 + k] * kf,
                                          static_cast<float>(ev));
                     if (!whole)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
+                        for (int k = 0; k < 4; ++k)
                             x[r0 + k] = there && pos >= sh_lo[r0 + k] && pos < sh_hi[r0 + k] ? x[r0 + k] : -INFINITY;
                     // the rows' maxima over the warp's keys
                     float mine = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const float m = warp_max(x[r0 + k]);
                         mine = lane == k ? m : mine;
                     }
-                    if (lane < 8)
+                    if (lane < 4)
                         sh_max[(par * R + r0 + lane) * 4 + warp] = mine;
                 }
                 tc_fence_before();
@@ -550,11 +546,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 float psum_new[R];
                 const float lf = pow2i(-ev);
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 8) {
+                for (int r0 = 0; r0 < R; r0 += 4) {
                     if (r0 >= live)
                         break;
 #pragma unroll
-                    for (int r = r0; r < r0 + 8; r += 2) {
+                    for (int r = r0; r < r0 + 4; r += 2) {
                         const float y0 = ex2_approx(x[r] - reference(r) + 8.f), y1 = ex2_approx(x[r + 1] - reference(r + 1) + 8.f);
                         psum_new[r] = y0 * lf;
                         psum_new[r + 1] = y1 * lf;
@@ -616,11 +612,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 if (j > 0)
                     add_tile(g);   // (and its product no longer reads the weights' place)
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 8) {
+                for (int r0 = 0; r0 < R; r0 += 4) {
                     if (r0 >= live)
                         break;
 #pragma unroll
-                    for (int r = r0; r < r0 + 8; ++r) {
+                    for (int r = r0; r < r0 + 4; ++r) {
                         psum[r] = psum_new[r];
 #pragma unroll
                         for (int term = 0; term < 3; ++term) {
@@ -639,19 +635,19 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 
             // ---- O and LSE of the unit's rows, or of this part of them
 #pragma unroll
-            for (int r0 = 0; r0 < R; r0 += 8) {
+            for (int r0 = 0; r0 < R; r0 += 4) {
                 if (r0 >= live)
                     break;
                 float mine = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     float v = l[r0 + k];
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1)
                         v += __shfl_xor_sync(0xffffffffu, v, d);
                     mine = lane == k ? v : mine;
                 }
-                if (lane < 8)
+                if (lane < 4)
                     sh_l[(r0 + lane) * 4 + warp] = mine;
             }
             sync();
@@ -659,13 +655,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const float4 l4 = *reinterpret_cast<const float4 *>(sh_l + tid * 4);
                 const float sum = tid < live ? (l4.x + l4.y) + (l4.z + l4.w) : 0.f;
                 sh_inv[tid] = sum == 0.f ? make_float2(0.f, -INFINITY)
-                                         : make_float2(1.f / sum, static_cast<float>(M) - 8.f + lg2_approx(sum));
+                                         : make_float2(__fdividef(1.f, sum), static_cast<float>(M) - 8.f + lg2_approx(sum));
             }
-            const int first_cta = cut ? range.owner(line.at) : cta;
-            const int last_cta = cut ? range.owner(line.at + span.tiles - 1) : cta;
-            const bool alone = first_cta == last_cta;
-            float *const part =
-                cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
             uint16_t *const o = static_cast<uint16_t *>(a.o);
             auto write_lse = [&](int r, float v) {
                 if (r < live)
@@ -679,9 +670,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     part[R * D + tid] = sh_inv[tid].y;
             }
 #pragma unroll
-            for (int r0 = 0; r0 < R; r0 += 8) {
+            for (int r0 = 0; r0 < R; r0 += 4) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const int r = r0 + k;
                     if (r >= live || !owns_d)
                         break;
