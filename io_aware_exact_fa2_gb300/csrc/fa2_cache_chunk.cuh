@@ -19,7 +19,7 @@
 //     4 warps   softmax: one row a thread, S from and P to tensor memory
 //     4 warps   codes from global memory to f16 operands in shared memory (swizzled),
 //               a tile ahead in registers
-//     1 thread  issues the products
+//     1 warp    issues the products
 // with two buffers of K, V and S each, and at D <= 128 two CTAs share an SM (256
 // columns of tensor memory each), so that one's exponentials run under the other's
 // products.  Work is cut and merged as in fa2_cache_line.cuh.
@@ -84,16 +84,14 @@ constexpr int CHUNK_ERR_SOFTMAX = 8 << 8, CHUNK_ERR_CONVERT = 9 << 8, CHUNK_ERR_
 constexpr uint32_t INFO_PAGE = 1u << 16;      // group word: key exponent byte, value exponent byte, this bit
 constexpr uint32_t FLAG_WHOLE = 1, FLAG_NAN = 2;
 
-// Sixteen codes as f16 into two 16-byte columns of a 128-byte-swizzled row.
-__device__ __forceinline__ void store_f16(uint32_t row_addr, int row, int c, bool swap, const uint4 &w)
+// Sixteen codes as f16 into two 16-byte columns of a 128-byte-swizzled row.  (Eight lanes
+// that store together have eight rows of one column: the swizzle spreads them over all banks.)
+__device__ __forceinline__ void store_f16(uint32_t row_addr, int row, int c, const uint4 &w)
 {
-    const uint32_t lo[4] = {e4m3x2_to_f16x2(w.x), e4m3x2_hi_to_f16x2(w.x), e4m3x2_to_f16x2(w.y), e4m3x2_hi_to_f16x2(w.y)};
-    const uint32_t hi[4] = {e4m3x2_to_f16x2(w.z), e4m3x2_hi_to_f16x2(w.z), e4m3x2_to_f16x2(w.w), e4m3x2_hi_to_f16x2(w.w)};
-    const uint32_t a0 = row_addr + ((c ^ (row & 7)) << 4), a1 = row_addr + (((c + 1) ^ (row & 7)) << 4);
-    // lanes of odd panels store their second half first: the other panels' lanes are in
-    // the banks of the first
-    ptx::st_shared_v4(swap ? a1 : a0, swap ? hi[0] : lo[0], swap ? hi[1] : lo[1], swap ? hi[2] : lo[2], swap ? hi[3] : lo[3]);
-    ptx::st_shared_v4(swap ? a0 : a1, swap ? lo[0] : hi[0], swap ? lo[1] : hi[1], swap ? lo[2] : hi[2], swap ? lo[3] : hi[3]);
+    ptx::st_shared_v4(row_addr + ((c ^ (row & 7)) << 4), e4m3x2_to_f16x2(w.x), e4m3x2_hi_to_f16x2(w.x), e4m3x2_to_f16x2(w.y),
+                      e4m3x2_hi_to_f16x2(w.y));
+    ptx::st_shared_v4(row_addr + (((c + 1) ^ (row & 7)) << 4), e4m3x2_to_f16x2(w.z), e4m3x2_hi_to_f16x2(w.z),
+                      e4m3x2_to_f16x2(w.w), e4m3x2_hi_to_f16x2(w.w));
 }
 
 // NaN codes among four: bit i for byte i.
@@ -162,42 +160,49 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
         // ============================================ one thread issues the products
         if constexpr (C::REG_SPLIT)
             setmaxnreg_dec<C::REG_ISSUE>();
-        if (warp == C::WARP_MMA && elect_one()) {
+        if (warp == C::WARP_MMA) {
+            // (all lanes wait: a lone lane would have to poll)
+            const bool leader = elect_one();
             const uint64_t desc_q = sdesc_sw128(base + C::OFF_Q, 16, 1024);
             const uint64_t desc_k = sdesc_sw128(base + C::OFF_K, 16, 1024);
             const uint64_t desc_v = sdesc_sw128(base + C::OFF_V, C::KV_PANEL, 1024);
-            auto wait = [&](int i, uint32_t parity) { return lone_wait(bar(i), parity, a.err, CHUNK_ERR_MMA | i, limit); };
             auto issue_s = [&](uint32_t g, bool last) -> bool {   // S = Q K^T of tile g
                 const uint32_t buf = g & 1;
-                if (!wait(C::BAR_K_FULL + buf, g >> 1 & 1))
+                if (!warp_wait(C::BAR_K_FULL + buf, g >> 1 & 1, CHUNK_ERR_MMA))
                     return false;
                 tc_fence_after();
-                const uint64_t dk = desc_k + (buf * C::KV_BYTES >> 4);
+                if (leader) {
+                    const uint64_t dk = desc_k + (buf * C::KV_BYTES >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tmem + C::TM_S + buf * TILE, desc_q + (((kk >> 2) * C::Q_PANEL + (kk & 3) * 32) >> 4),
-                           dk + (((kk >> 2) * C::KV_PANEL + (kk & 3) * 32) >> 4), C::idesc(TILE, false), kk > 0);
-                mma_commit(bar(C::BAR_S_FULL + buf));
-                mma_commit(bar(C::BAR_K_EMPTY + buf));
-                if (last)
-                    mma_commit(bar(C::BAR_Q_EMPTY));
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(tmem + C::TM_S + buf * TILE, desc_q + (((kk >> 2) * C::Q_PANEL + (kk & 3) * 32) >> 4),
+                               dk + (((kk >> 2) * C::KV_PANEL + (kk & 3) * 32) >> 4), C::idesc(TILE, false), kk > 0);
+                    mma_commit(bar(C::BAR_S_FULL + buf));
+                    mma_commit(bar(C::BAR_K_EMPTY + buf));
+                    if (last)
+                        mma_commit(bar(C::BAR_Q_EMPTY));
+                }
+                __syncwarp();
                 return true;
             };
             auto issue_pv = [&](uint32_t g, bool start) -> bool {   // O += P V of tile g
                 const uint32_t buf = g & 1;
-                if (!wait(C::BAR_P_FULL + buf, g >> 1 & 1) || !wait(C::BAR_V_FULL + buf, g >> 1 & 1))
-                    return false;
                 // a unit's first product overwrites O: the one before has been read out
-                if (start && unit > 0 && !wait(C::BAR_O_FREE, (unit - 1) & 1))
+                if (!warp_wait(C::BAR_V_FULL + buf, g >> 1 & 1, CHUNK_ERR_MMA) ||
+                    !warp_wait(C::BAR_P_FULL + buf, g >> 1 & 1, CHUNK_ERR_MMA) ||
+                    (start && unit > 0 && !warp_wait(C::BAR_O_FREE, (unit - 1) & 1, CHUNK_ERR_MMA)))
                     return false;
                 tc_fence_after();
-                const uint64_t dv = desc_v + (buf * C::KV_BYTES >> 4);
+                if (leader) {
+                    const uint64_t dv = desc_v + (buf * C::KV_BYTES >> 4);
 #pragma unroll
-                for (int kk = 0; kk < TILE / 16; ++kk)
-                    mma_ts(tmem + C::TM_O, tmem + C::TM_S + buf * TILE + kk * 8, dv + (kk * 16 * 128 >> 4),
-                           C::idesc(D, true), !start || kk > 0);
-                mma_commit(bar(C::BAR_O_DONE));
-                mma_commit(bar(C::BAR_V_EMPTY + buf));
+                    for (int kk = 0; kk < TILE / 16; ++kk)
+                        mma_ts(tmem + C::TM_O, tmem + C::TM_S + buf * TILE + kk * 8, dv + (kk * 16 * 128 >> 4),
+                               C::idesc(D, true), !start || kk > 0);
+                    mma_commit(bar(C::BAR_O_DONE));
+                    mma_commit(bar(C::BAR_V_EMPTY + buf));
+                }
+                __syncwarp();
                 return true;
             };
             bool ok = true;
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 int tile0, tile1;
                 part_of(tile0, tile1);
                 const int n = tile1 - tile0;
-                ok = wait(C::BAR_Q_FULL, unit & 1);
+                ok = warp_wait(C::BAR_Q_FULL, unit & 1, CHUNK_ERR_MMA);
                 for (int j = 0; j < 2 && j < n && ok; ++j)
                     ok = issue_s(it + j, j == n - 1);
                 for (int j = 0; j < n && ok; ++j) {
@@ -217,18 +222,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 ++unit;
             } while (ok && next_unit());
             // nothing issued is still running when tensor memory is given back
-            mma_commit(bar(C::BAR_DRAIN));
-            lone_wait(bar(C::BAR_DRAIN), 0, a.err, CHUNK_ERR_DRAIN, limit);
+            if (leader)
+                mma_commit(bar(C::BAR_DRAIN));
+            __syncwarp();
+            warp_wait(C::BAR_DRAIN, 0, CHUNK_ERR_DRAIN);
         }
-        __syncwarp();
     } else if (warp >= C::WARP_CONVERT) {
         // ============================================ codes -> f16 operands
-        constexpr int COLS = D / 16;                     // 16-byte pieces of a row
-        constexpr int STEP = 128 / COLS, NL = TILE / STEP;   // rows that 128 threads cover; pieces a thread takes of K
-        const int ct = tid - 32 * C::WARP_CONVERT, col = ct % COLS, row0 = ct / COLS;
-        const uint32_t piece = base + (col >> 2) * C::KV_PANEL;
-        const int c0 = (col & 3) * 2;
-        const bool swap = (col >> 2) & 1;
+        // A warp takes blocks of 8 rows by 64 bytes: rows 8 w .. and 8 (w + 4) .. of every
+        // panel, so two 16-key groups a tile.
+        constexpr int NL = D / 32;                       // 16-byte pieces a thread takes of K
+        const int w = warp - C::WARP_CONVERT, c = lane >> 3;
+        const int row0 = w * 8 + (lane & 7);             // piece i: row row0 + 32 (i & 1), panel i / 2
+        auto piece = [&](int off, uint32_t buf, int i) {
+            return base + off + buf * C::KV_BYTES + (i >> 1) * C::KV_PANEL + (row0 + 32 * (i & 1)) * 128;
+        };
         bool ok = true;
         do {
             int tile0, tile1;
@@ -254,8 +262,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
             uint32_t sc_now = scale_batch(id_now), sc_next = scale_batch(id_next);
 
             uint4 k_reg[NL], v_reg[NL];
-            uint32_t info = 0;                           // lane i < GROUPS: group i of the loaded tile
-            auto load = [&](int j) {
+            uint32_t info = 0;                           // lane i < GROUPS: group i of the tile to come
+            int id_row[2];                               // pages of this thread's two rows
+            auto advance = [&](int j) {                  // to tile j
                 if (j > 0 && (j & 7) == 0) {
                     id_now = id_next;
                     id_next = id_after;
@@ -265,24 +274,26 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 }
                 info = __shfl_sync(0xffffffffu, sc_now, (j & 7) * GROUPS + (lane & (GROUPS - 1)));
 #pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const int row = row0 + i * STEP;     // (one group a warp)
-                    const int id = __shfl_sync(0xffffffffu, id_now, (j & 7) * GROUPS + (row >> 4));
-                    const int pos = from + j * TILE + row;
-                    uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-                    // positions that no row of the block sees are zeros
-                    if (id >= 0 && pos >= line.span.lo && pos < stop) {
-                        const int slot = pos & ((1 << a.c.page_shift) - 1);
-                        kw = __ldg(reinterpret_cast<const uint4 *>(a.c.k.codes + id * a.c.k.s_page + h * a.c.k.s_head +
-                                                                   slot * a.c.k.s_slot + col * 16));
-                        vw = __ldg(reinterpret_cast<const uint4 *>(a.c.v.codes + id * a.c.v.s_page + h * a.c.v.s_head +
-                                                                   slot * a.c.v.s_slot + col * 16));
-                    }
-                    k_reg[i] = kw;
-                    v_reg[i] = vw;
-                }
+                for (int r = 0; r < 2; ++r)
+                    id_row[r] = __shfl_sync(0xffffffffu, id_now, (j & 7) * GROUPS + (w >> 1) + 2 * r);
             };
-            load(0);
+            auto load = [&](uint4 (&reg)[NL], const Half &half, int j) {
+                const uint8_t *p[2];
+                bool seen[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int pos = from + j * TILE + row0 + 32 * r, slot = pos & ((1 << a.c.page_shift) - 1);
+                    // positions that no row of the block sees are zeros
+                    seen[r] = id_row[r] >= 0 && pos >= line.span.lo && pos < stop;
+                    p[r] = half.codes + id_row[r] * half.s_page + h * half.s_head + slot * half.s_slot + c * 16;
+                }
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    reg[i] = seen[i & 1] ? __ldg(reinterpret_cast<const uint4 *>(p[i & 1] + (i >> 1) * 64)) : make_uint4(0, 0, 0, 0);
+            };
+            advance(0);
+            load(k_reg, a.c.k, 0);
+            load(v_reg, a.c.v, 0);
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t g = it + j, buf = g & 1, par = (g >> 1 & 1) ^ 1, slot = g & 3;
                 const int pos0 = from + j * TILE;
@@ -298,7 +309,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                     uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + slot * C::NAN_BYTES);
 #pragma unroll
                     for (int i = 0; i < NL; ++i) {
-                        const int row = row0 + i * STEP;
+                        const int row = row0 + 32 * (i & 1);
                         const uint32_t sc = __shfl_sync(0xffffffffu, info, row >> 4);
                         uint32_t m = nan_bits(v_reg[i].x) | nan_bits(v_reg[i].y) << 4 | nan_bits(v_reg[i].z) << 8 |
                                      nan_bits(v_reg[i].w) << 12;
@@ -309,34 +320,33 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                             v_reg[i] = make_uint4(without_nan(v_reg[i].x), without_nan(v_reg[i].y),
                                                   without_nan(v_reg[i].z), without_nan(v_reg[i].w));
                         nan |= m != 0;
-                        map[row * (D / 16) + col] = static_cast<uint16_t>(m);
+                        map[row * (D / 16) + (i >> 1) * 4 + c] = static_cast<uint16_t>(m);
                     }
                     nan = __any_sync(0xffffffffu, nan);
                 }
                 uint32_t *const words = reinterpret_cast<uint32_t *>(smem + C::OFF_INFO + slot * C::INFO_BYTES);
-                if (warp == C::WARP_CONVERT && lane < GROUPS)
+                if (w == 0 && lane < GROUPS)
                     words[lane] = info;
                 if (lane == 0)   // flags, one byte a warp
-                    reinterpret_cast<uint8_t *>(words + GROUPS)[warp - C::WARP_CONVERT] =
-                        (whole ? FLAG_WHOLE : 0) | (nan ? FLAG_NAN : 0);
+                    reinterpret_cast<uint8_t *>(words + GROUPS)[w] = (whole ? FLAG_WHOLE : 0) | (nan ? FLAG_NAN : 0);
 #pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const int row = row0 + i * STEP;
-                    store_f16(piece + C::OFF_K + buf * C::KV_BYTES + row * 128, row, c0, swap, k_reg[i]);
-                }
+                for (int i = 0; i < NL; ++i)
+                    store_f16(piece(C::OFF_K, buf, i), row0, c * 2, k_reg[i]);
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_K_FULL + buf);
+                if (j + 1 < n) {   // the next tile's keys come in while these values are converted
+                    advance(j + 1);
+                    load(k_reg, a.c.k, j + 1);
+                }
                 if (g >= 2 && !(ok = warp_wait(C::BAR_V_EMPTY + buf, par, CHUNK_ERR_CONVERT)))
                     break;
 #pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const int row = row0 + i * STEP;
-                    store_f16(piece + C::OFF_V + buf * C::KV_BYTES + row * 128, row, c0, swap, v_reg[i]);
-                }
+                for (int i = 0; i < NL; ++i)
+                    store_f16(piece(C::OFF_V, buf, i), row0, c * 2, v_reg[i]);
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_V_FULL + buf);
                 if (j + 1 < n)
-                    load(j + 1);
+                    load(v_reg, a.c.v, j + 1);
             }
             it += n;
         } while (ok && next_unit());
@@ -493,28 +503,35 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 }
                 // weights, over the first half of this S buffer as f16 pairs
                 const float ref = M == -INFINITY ? 0.f : M;
-                uint32_t p[32];
 #pragma unroll
-                for (int q = 0; q < GROUPS; ++q) {
-                    const uint32_t *r = q < 2 ? r0 + q * CHUNK : r1 + (q - 2) * CHUNK;
-                    const float add = static_cast<float>(ev[q]) + 6.f - ref;
-                    float sum0 = 0.f, sum1 = 0.f;
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int k = 0; k < CHUNK; k += 2) {
-                        float x0 = fmaf(__uint_as_float(r[k]), c[q], add), x1 = fmaf(__uint_as_float(r[k + 1]), c[q], add);
-                        if (!whole) {   // (hidden scores stay -inf whatever the scale)
-                            x0 = r[k] == 0xff800000u ? -INFINITY : x0;
-                            x1 = r[k + 1] == 0xff800000u ? -INFINITY : x1;
+                    for (int q = 0; q < GROUPS / 2; ++q) {
+                        const uint32_t *r = (half ? r1 : r0) + q * CHUNK;
+                        const int grp = half * 2 + q;
+                        const float add = static_cast<float>(ev[grp]) + 6.f - ref;
+                        const uint64_t c2 = f32x2(c[grp], c[grp]), add2 = f32x2(add, add);
+                        uint64_t sum2 = 0;
+#pragma unroll
+                        for (int k = 0; k < CHUNK; k += 2) {
+                            float x0, x1;
+                            unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, add2), x0, x1);
+                            if (!whole) {   // (hidden scores stay -inf whatever the scale)
+                                x0 = r[k] == 0xff800000u ? -INFINITY : x0;
+                                x1 = r[k + 1] == 0xff800000u ? -INFINITY : x1;
+                            }
+                            x0 = ex2_approx(x0);
+                            x1 = ex2_approx(x1);
+                            sum2 = add_f32x2(sum2, f32x2(x0, x1));
+                            p[q * 8 + k / 2] = pack_f16x2(x0, x1);
                         }
-                        x0 = ex2_approx(x0);
-                        x1 = ex2_approx(x1);
-                        sum0 += x0;
-                        sum1 += x1;
-                        p[q * 8 + k / 2] = pack_f16x2(x0, x1);
+                        float sum0, sum1;
+                        unpack_f32x2(sum2, sum0, sum1);
+                        l = fmaf(sum0 + sum1, pow2i(-ev[grp]), l);
                     }
-                    l = fmaf(sum0 + sum1, pow2i(-ev[q]), l);
+                    tmem_st16(s_addr + half * 16, p);
                 }
-                tmem_st32(s_addr, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(C::BAR_P_FULL + buf);
