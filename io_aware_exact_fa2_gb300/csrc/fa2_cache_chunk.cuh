@@ -54,7 +54,7 @@ struct ChunkCfg {
     static constexpr int OFF_Q = 0, OFF_K = Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES;
     // rings of four: a tile's group scales and flags, its NaN values by key
     static constexpr int NAN_WORDS = D / 32;
-    static constexpr int OFF_INFO = OFF_V + 2 * KV_BYTES, INFO_BYTES = 32;
+    static constexpr int OFF_INFO = OFF_V + 2 * KV_BYTES, INFO_BYTES = GROUPS * 16 + 16;
     static constexpr int OFF_NAN = OFF_INFO + 4 * INFO_BYTES, NAN_BYTES = TILE * NAN_WORDS * 4;
     static constexpr int OFF_BAR = OFF_NAN + 4 * NAN_BYTES;
     static constexpr int NUM_BAR = 18;
@@ -81,7 +81,9 @@ constexpr int CHUNK_ERR_SOFTMAX = 8 << 8, CHUNK_ERR_CONVERT = 9 << 8, CHUNK_ERR_
 #ifdef __CUDACC__
 
 // What the converting warps tell the softmax warps of a tile.
-constexpr uint32_t INFO_PAGE = 1u << 16;      // group word: key exponent byte, value exponent byte, this bit
+// For each group of 16 keys: 2^ek, ev, 2^-ev, and a word of the key and value scales' bytes
+// and this bit (0: no page); then a flag byte from each converting warp.
+constexpr uint32_t INFO_PAGE = 1u << 16;
 constexpr uint32_t FLAG_WHOLE = 1, FLAG_NAN = 2;
 
 // Sixteen codes as f16 into two 16-byte columns of a 128-byte-swizzled row.  (Eight lanes
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 const int pos0 = from + j * TILE;
                 if (g >= 2 && !(ok = warp_wait(C::BAR_K_EMPTY + buf, par, CHUNK_ERR_CONVERT)))
                     break;
-                const bool pages = __all_sync(0xffffffffu, (info & INFO_PAGE) && (info >> 8 & 255) != 255);
+                const bool pages = __all_sync(0xffffffffu, (info & INFO_PAGE) && (info & 255) != 255 && (info >> 8 & 255) != 255);
                 const bool whole = pages && pos0 >= all_lo && pos0 + TILE <= all_hi;
                 bool nan = false;
                 if (!whole) {
@@ -325,10 +327,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                     nan = __any_sync(0xffffffffu, nan);
                 }
                 uint32_t *const words = reinterpret_cast<uint32_t *>(smem + C::OFF_INFO + slot * C::INFO_BYTES);
-                if (w == 0 && lane < GROUPS)
-                    words[lane] = info;
+                if (w == 0 && lane < GROUPS) {
+                    // (a NaN scale: the softmax warps go by its byte)
+                    const int kb = info & 255, vb = info >> 8 & 255;
+                    const int ek = kb == 255 ? 0 : kb - 127, ev = vb == 255 ? 0 : vb - 127;
+                    reinterpret_cast<float4 *>(words)[lane] =
+                        make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev), __uint_as_float(info));
+                }
                 if (lane == 0)   // flags, one byte a warp
-                    reinterpret_cast<uint8_t *>(words + GROUPS)[w] = (whole ? FLAG_WHOLE : 0) | (nan ? FLAG_NAN : 0);
+                    reinterpret_cast<uint8_t *>(words + GROUPS * 4)[w] = (whole ? FLAG_WHOLE : 0) | (nan ? FLAG_NAN : 0);
 #pragma unroll
                 for (int i = 0; i < NL; ++i)
                     store_f16(piece(C::OFF_K, buf, i), row0, c * 2, k_reg[i]);
@@ -414,6 +421,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 warp_arrive(C::BAR_Q_FULL);
             }
 
+            const float scale_row = scale_log2 * pow2i(e);
             float M = -INFINITY, l = 0.f;
             uint32_t nan[C::NAN_WORDS];   // values of O that a visible NaN value makes NaN
 #pragma unroll
@@ -428,17 +436,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 uint32_t r0[32], r1[32];
                 tmem_ld32(s_addr, r0);
                 tmem_ld32(s_addr + 32, r1);
-                const uint4 info = *reinterpret_cast<const uint4 *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES);
-                const uint32_t flags = *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES + 16);
-                const uint32_t words[GROUPS] = {info.x, info.y, info.z, info.w};
-                float c[GROUPS];          // x = S * c
-                int ev[GROUPS];
+                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES);
+                const uint32_t flags = __float_as_uint(info[GROUPS].x);
+                float c[GROUPS], ev[GROUPS], lf[GROUPS];      // x = S * c
 #pragma unroll
                 for (int q = 0; q < GROUPS; ++q) {
-                    const int ek = static_cast<int>(words[q] & 255) - 127;
-                    c[q] = ek == 128 ? __uint_as_float(0x7fc00000u) : scale_log2 * pow2i(e + ek);
-                    ev[q] = static_cast<int>(words[q] >> 8 & 255) - 127;
-                    ev[q] = ev[q] == 128 ? 0 : ev[q];
+                    const float4 f = info[q];
+                    c[q] = fmaxf(scale_row * f.x, 1.17549435e-38f);   // (not 0: a hidden score is -inf * c)
+                    ev[q] = f.y;
+                    lf[q] = f.z;
                 }
                 tmem_ld_wait(r0);
                 tmem_ld_wait(r1);
@@ -446,10 +452,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 if (!whole) {             // scores that the row does not see
                     const int pos0 = from + j * TILE;
 #pragma unroll
-                    for (int k = 0; k < TILE; ++k) {
-                        uint32_t &x = k < 32 ? r0[k & 31] : r1[k & 31];
-                        const bool see = pos0 + k >= lo && pos0 + k < hi && (words[k / CHUNK] & INFO_PAGE);
-                        x = see ? x : 0xff800000u;
+                    for (int q = 0; q < GROUPS; ++q) {
+                        const uint32_t word = __float_as_uint(info[q].w);
+                        const bool page = word & INFO_PAGE, nan_scale = (word & 255) == 255;
+#pragma unroll
+                        for (int k = q * CHUNK; k < (q + 1) * CHUNK; ++k) {
+                            uint32_t &x = k < 32 ? r0[k & 31] : r1[k & 31];
+                            const bool see = page && pos0 + k >= lo && pos0 + k < hi;
+                            x = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : x;
+                        }
                     }
                     if (flags & 0x02020202u) {
                         const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
@@ -471,8 +482,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                     for (int k = 1; k < 15; k += 2)
                         t = max3(t, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
                     t = fmaxf(t, __uint_as_float(r[15]));
-                    // (-inf times a scale that underflowed to zero would be NaN, which fmaxf drops)
-                    top = fmaxf(top, t * c[q] + static_cast<float>(ev[q]));
+                    top = fmaxf(top, fmaf(t, c[q], ev[q]));
                 }
                 const bool raise = top > M + 8.f, any = __any_sync(0xffffffffu, raise);
                 float f = 1.f;
@@ -510,17 +520,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                     for (int q = 0; q < GROUPS / 2; ++q) {
                         const uint32_t *r = (half ? r1 : r0) + q * CHUNK;
                         const int grp = half * 2 + q;
-                        const float add = static_cast<float>(ev[grp]) + 6.f - ref;
+                        const float add = ev[grp] + 6.f - ref;
                         const uint64_t c2 = f32x2(c[grp], c[grp]), add2 = f32x2(add, add);
                         uint64_t sum2 = 0;
 #pragma unroll
                         for (int k = 0; k < CHUNK; k += 2) {
                             float x0, x1;
                             unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, add2), x0, x1);
-                            if (!whole) {   // (hidden scores stay -inf whatever the scale)
-                                x0 = r[k] == 0xff800000u ? -INFINITY : x0;
-                                x1 = r[k + 1] == 0xff800000u ? -INFINITY : x1;
-                            }
                             x0 = ex2_approx(x0);
                             x1 = ex2_approx(x1);
                             sum2 = add_f32x2(sum2, f32x2(x0, x1));
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                         }
                         float sum0, sum1;
                         unpack_f32x2(sum2, sum0, sum1);
-                        l = fmaf(sum0 + sum1, pow2i(-ev[grp]), l);
+                        l = fmaf(sum0 + sum1, lf[grp], l);
                     }
                     tmem_st16(s_addr + half * 16, p);
                 }

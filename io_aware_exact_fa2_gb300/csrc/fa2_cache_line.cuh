@@ -134,8 +134,10 @@ struct Range {
 template <class C>
 __device__ __forceinline__ long long tiles_of(const AttnArgs &a, const Seq &s)
 {
-    long long n = 0;
     const int blocks = row_blocks<C>(a, s);
+    if (!a.causal)   // every block sees all keys
+        return blocks ? static_cast<long long>(blocks) * (span_of<C>(a, s, 0).tiles + C::UNIT_COST) : 0;
+    long long n = 0;
     for (int rb = 0; rb < blocks; ++rb)
         n += span_of<C>(a, s, rb).tiles + C::UNIT_COST;
     return n;
