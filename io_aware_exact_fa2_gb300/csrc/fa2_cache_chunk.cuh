@@ -2,32 +2,36 @@
 // (fa2_cache_attn in include/fa2_cache.h): blocks of 128 rows on the 5th-generation
 // tensor cores.
 //
-// Mathematics.  As in fa2_cache_attn.cuh, rows are the tokens of a sequence times the
-// query heads that share a key/value head, codes and rows of Q (times a power of two)
-// are exact in f16, and one accumulator takes pages of any strength: for key j of a
-// page with exponents ek, ev
-//     x_j = S_j * scale * log2 e * 2^ek,   p'_j = 2^(x_j + ev - M + 6)   (f16 for P V)
-//     O += P' V,   l += 2^-ev sum p'       M: running maximum of x + ev
-// so both exponents ride in the one multiply-add before the exponential, at no cost.
-// M is raised only when a tile exceeds it by more than 2^8: p' stays within 2^14.
+// Mathematics.  As in fa2_cache_step.cuh, rows are the tokens of a sequence times the query
+// heads that share a key/value head.  The scores are e4m3 products, the cache's codes as
+// they are and q as two terms,
+//     q 2^-e = q0 + q1          (e: largest magnitude of the row in [224, 448))
+// exact but for elements below 2^-9 of their row's largest, which are off by up to 2^-17 of
+// that.  For key j of a page with exponents ek, ev
+//     x_j = S_j * scale * log2 e * 2^(e + ek),   p'_j = 2^(x_j + ev - M + 6)
+//     O += P' V,   l += 2^-ev sum p'             M: running maximum of x + ev
+// so both exponents ride in the one multiply-add before the exponential, at no cost, and one
+// accumulator takes pages of any strength.  P' is f16 (two terms of e4m3 would not span a
+// long context's weights) and V is converted to f16, exactly.  M is raised only when a tile
+// exceeds it by more than 2^8: p' stays within 2^14.
 //
-// What bounds it.  4 D operations a (row, key) pair against D / 64 cache bytes a row
-// and key: the tensor pipe.  Two f16 products of 128 rows x 64 keys x D = 128 take
-// some 540 cycles; the exponentials and the rest of the softmax cost about as much
-// issue time, and each code has to be converted once a block of rows.  So the three
-// run on warps of their own,
+// What bounds it.  4 D operations a (row, key) pair against D / 64 cache bytes a row and
+// key: the tensor pipe.  (Two e4m3 products take the time of one of f16, and K needs no
+// conversion.)  128 rows x 64 keys x D = 128 take some 540 cycles; the exponentials and the
+// rest of the softmax cost about as much issue time.  So the work has warps of its own,
 //     4 warps   softmax: one row a thread, S from and P to tensor memory
-//     4 warps   codes from global memory to f16 operands in shared memory (swizzled),
-//               a tile ahead in registers
+//     4 warps   values' codes to f16 operands in shared memory (swizzled)
 //     1 warp    issues the products
-// with two buffers of K, V and S each, and at D <= 128 two CTAs share an SM (256
-// columns of tensor memory each), so that one's exponentials run under the other's
-// products.  Work is cut and merged as in fa2_cache_line.cuh.
+//     1 warp    pages into shared memory by TMA
+// and at D <= 128 two CTAs share an SM (256 columns of tensor memory each), so that one's
+// exponentials run under the other's products.  Work is cut and merged as in
+// fa2_cache_line.cuh.
 #pragma once
 
 #include <atomic>
 
 #include "fa2_cache_line.cuh"
+#include "fa2_cache_tile.cuh"
 
 namespace fa2 {
 namespace cache {
@@ -38,53 +42,52 @@ struct ChunkCfg {
     static constexpr int R = 128;                    // query rows of a unit
     static constexpr int TILE = 64;                  // keys
     static constexpr int UNIT_COST = 4, MIN_TILES = 4;   // see fa2_cache_line.cuh
-    static constexpr int ALIGN = CHUNK;              // where a unit's first tile may begin
+    static constexpr int ALIGN = TILE;               // a tile begins at a multiple
     static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
-    static constexpr int WARP_CONVERT = 4, WARP_MMA = 8;
-    static constexpr int T = 32 * 12;                // (the last warpgroup: one issuing warp and three idle ones)
+    static constexpr int WARP_CONVERT = 4, WARP_MMA = 8, WARP_LOAD = 9;
+    static constexpr int T = 32 * 12;                // (the last warpgroup: two idle warps)
     // With two CTAs an SM the launch leaves 80 registers a thread, 240 for the three
-    // warpgroups' lanes together: the softmax rises, the issuing warpgroup gives.
+    // warpgroups' lanes together: the softmax rises, the others give.
     static constexpr bool REG_SPLIT = CTAS == 2;
-    static constexpr int REG_SOFTMAX = 120, REG_CONVERT = 80, REG_ISSUE = 40;
+    static constexpr int REG_SOFTMAX = 128, REG_CONVERT = 64, REG_ISSUE = 48;
     static_assert(REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 3 * 80, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
-    static constexpr int Q_PANEL = R * 128, KV_PANEL = TILE * 128;   // 64 columns of f16, 128-byte rows
-    static constexpr int Q_BYTES = D / 64 * Q_PANEL, KV_BYTES = D / 64 * KV_PANEL;
-    static constexpr int OFF_Q = 0, OFF_K = Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES;
-    // rings of four: a tile's group scales and flags, its NaN values by key
+    static constexpr int ROW = D == 64 ? 64 : 128;   // bytes of a row of codes: its swizzle span
+    static constexpr int PANELS = D / ROW, PANEL = TILE * ROW;       // of a stage of codes
+    static constexpr int STAGE = TILE * D, KS = 2, VS = 3;           // stages of keys, of values
+    static constexpr int Q_PANEL = R * ROW, Q_TERM = R * D;          // Q: two terms of codes
+    static constexpr int V_PANEL = TILE * 128, V_BYTES = TILE * D * 2;   // V in f16: 64 columns, 128-byte rows
+    static constexpr int OFF_Q = 0, OFF_V = 2 * Q_TERM, OFF_K = OFF_V + 2 * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
+    // a ring of eight tiles' group scales; of four tiles' NaN flags and NaN values by key
     static constexpr int NAN_WORDS = D / 32;
-    static constexpr int OFF_INFO = OFF_V + 2 * KV_BYTES, INFO_BYTES = GROUPS * 16 + 16;
-    static constexpr int OFF_NAN = OFF_INFO + 4 * INFO_BYTES, NAN_BYTES = TILE * NAN_WORDS * 4;
+    static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16;
+    static constexpr int OFF_FLAGS = OFF_INFO + 8 * INFO_BYTES;
+    static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
     static constexpr int OFF_BAR = OFF_NAN + 4 * NAN_BYTES;
-    static constexpr int NUM_BAR = 18;
+    static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_V_FULL = 2, BAR_V_EMPTY = 4, BAR_S_FULL = 6, BAR_P_FULL = 8,
+                         BAR_O_DONE = 10, BAR_O_FREE = 11, BAR_GROUP = 12, BAR_DRAIN = 13, BAR_K_FULL = 14,
+                         BAR_K_EMPTY = BAR_K_FULL + KS, BAR_RAW_FULL = BAR_K_EMPTY + KS, BAR_RAW_EMPTY = BAR_RAW_FULL + VS,
+                         NUM_BAR = BAR_RAW_EMPTY + VS;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // 1024: operand alignment
 
     static constexpr int TM_S = 0, TM_O = 2 * TILE;
     static constexpr int TMEM_COLS = D <= 128 ? 256 : 512;
 
-    static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_K_FULL = 2, BAR_K_EMPTY = 4, BAR_V_FULL = 6, BAR_V_EMPTY = 8,
-                         BAR_S_FULL = 10, BAR_P_FULL = 12, BAR_O_DONE = 14, BAR_O_FREE = 15, BAR_GROUP = 16, BAR_DRAIN = 17;
-
     // kind::f16 with f16 A and B (formats 0), fp32 accumulator
     static constexpr uint32_t idesc(int n, bool b_mn)
     {
         return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(R >> 4) << 24);
     }
-    static_assert(CTAS * SMEM_BYTES <= 227 * 1024 && CTAS * TMEM_COLS <= 512 && 2 * TILE + D <= TMEM_COLS, "an SM holds CTAS of them");
+    static_assert(CTAS * (SMEM_BYTES + 1024 + 512) <= 228 * 1024 && CTAS * TMEM_COLS <= 512 && 2 * TILE + D <= TMEM_COLS, "an SM holds CTAS of them");
 };
 
 // Error codes of waits that ran out (bits 8-11 the waiting role).
-constexpr int CHUNK_ERR_SOFTMAX = 8 << 8, CHUNK_ERR_CONVERT = 9 << 8, CHUNK_ERR_MMA = 10 << 8, CHUNK_ERR_DRAIN = 11 << 8;
+constexpr int CHUNK_ERR_SOFTMAX = 8 << 8, CHUNK_ERR_CONVERT = 9 << 8, CHUNK_ERR_MMA = 10 << 8, CHUNK_ERR_LOAD = 11 << 8,
+              CHUNK_ERR_DRAIN = 7 << 8;
 
 #ifdef __CUDACC__
-
-// What the converting warps tell the softmax warps of a tile.
-// For each group of 16 keys: 2^ek, ev, 2^-ev, and a word of the key and value scales' bytes
-// and this bit (0: no page); then a flag byte from each converting warp.
-constexpr uint32_t INFO_PAGE = 1u << 16;
-constexpr uint32_t FLAG_WHOLE = 1, FLAG_NAN = 2;
 
 // Sixteen codes as f16 into two 16-byte columns of a 128-byte-swizzled row.  (Eight lanes
 // that store together have eight rows of one column: the swizzle spreads them over all banks.)
@@ -104,7 +107,9 @@ __device__ __forceinline__ uint32_t nan_bits(uint32_t w)
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, const Parts parts)
+__global__ void __launch_bounds__(C::T, C::CTAS)
+    chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const AttnArgs a,
+                 const Parts parts)
 {
     using namespace ptx;
     constexpr int D = C::D, R = C::R, TILE = C::TILE, GROUPS = C::GROUPS;
@@ -125,8 +130,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
     if (tid == 0) {
         for (int i = 0; i < C::NUM_BAR; ++i) {
-            const bool by_warps = i == C::BAR_Q_FULL || i / 2 == C::BAR_K_FULL / 2 || i / 2 == C::BAR_V_FULL / 2 ||
-                                  i / 2 == C::BAR_P_FULL / 2 || i == C::BAR_O_FREE || i == C::BAR_GROUP;
+            const bool by_warps = i == C::BAR_Q_FULL || i / 2 == C::BAR_V_FULL / 2 || i / 2 == C::BAR_P_FULL / 2 ||
+                                  i == C::BAR_O_FREE || i == C::BAR_GROUP || i >= C::BAR_RAW_EMPTY;
             mbar_init(bar(i), by_warps ? 4 : 1);
         }
         fence_mbar_init();
@@ -155,6 +160,19 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
         tile1 = cut && end < line.at + line.span.tiles ? static_cast<int>(end - line.at) : line.span.tiles;
     };
     auto next_unit = [&]() { return line.next(a) && line.at < end; };
+    // a group's scales (see the loading warp); whether every row sees every key of tile g
+    auto group_word = [](const uint8_t *smem, uint32_t g, int q) {
+        return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES)[q * 4 + 3];
+    };
+    auto all_whole = [&](const uint8_t *smem, uint32_t g, int pos0, int all_lo, int all_hi) {
+        bool whole = pos0 >= all_lo && pos0 + TILE <= all_hi;
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q) {
+            const uint32_t sc = group_word(smem, g, q);
+            whole &= (sc & PAGE_BIT) && (sc & 255) != 255 && (sc >> 8 & 255) != 255;
+        }
+        return whole;
+    };
     uint32_t it = 0;       // tiles before the present unit's first: buffers alternate by tile
     uint32_t unit = 0;
 
@@ -165,22 +183,28 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
         if (warp == C::WARP_MMA) {
             // (all lanes wait: a lone lane would have to poll)
             const bool leader = elect_one();
-            const uint64_t desc_q = sdesc_sw128(base + C::OFF_Q, 16, 1024);
-            const uint64_t desc_k = sdesc_sw128(base + C::OFF_K, 16, 1024);
-            const uint64_t desc_v = sdesc_sw128(base + C::OFF_V, C::KV_PANEL, 1024);
+            const uint64_t desc_q = D == 64 ? sdesc_sw64(base + C::OFF_Q, 16, 512) : sdesc_sw128(base + C::OFF_Q, 16, 1024);
+            const uint64_t desc_k = D == 64 ? sdesc_sw64(base + C::OFF_K, 16, 512) : sdesc_sw128(base + C::OFF_K, 16, 1024);
+            const uint64_t desc_v = sdesc_sw128(base + C::OFF_V, C::V_PANEL, 1024);
             auto issue_s = [&](uint32_t g, bool last) -> bool {   // S = Q K^T of tile g
-                const uint32_t buf = g & 1;
-                if (!warp_wait(C::BAR_K_FULL + buf, g >> 1 & 1, CHUNK_ERR_MMA))
+                const uint32_t stage = g % C::KS;
+                if (!warp_wait(C::BAR_K_FULL + stage, g / C::KS & 1, CHUNK_ERR_MMA))
                     return false;
                 tc_fence_after();
                 if (leader) {
-                    const uint64_t dk = desc_k + (buf * C::KV_BYTES >> 4);
+                    const uint64_t dk = desc_k + (stage * C::STAGE >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        mma_ss(tmem + C::TM_S + buf * TILE, desc_q + (((kk >> 2) * C::Q_PANEL + (kk & 3) * 32) >> 4),
-                               dk + (((kk >> 2) * C::KV_PANEL + (kk & 3) * 32) >> 4), C::idesc(TILE, false), kk > 0);
-                    mma_commit(bar(C::BAR_S_FULL + buf));
-                    mma_commit(bar(C::BAR_K_EMPTY + buf));
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int kk = 0; kk < D / 32; ++kk) {
+                            const int panel = kk * 32 / C::ROW, col = kk * 32 % C::ROW;
+                            mma_ss<true>(tmem + C::TM_S + (g & 1) * TILE,
+                                         desc_q + ((term * C::Q_TERM + panel * C::Q_PANEL + col) >> 4),
+                                         dk + ((panel * C::PANEL + col) >> 4), idesc_e4m3_f32(R, TILE, false, false),
+                                         term > 0 || kk > 0);
+                        }
+                    mma_commit(bar(C::BAR_S_FULL + (g & 1)));
+                    mma_commit(bar(C::BAR_K_EMPTY + stage));
                     if (last)
                         mma_commit(bar(C::BAR_Q_EMPTY));
                 }
@@ -196,7 +220,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                     return false;
                 tc_fence_after();
                 if (leader) {
-                    const uint64_t dv = desc_v + (buf * C::KV_BYTES >> 4);
+                    const uint64_t dv = desc_v + (buf * C::V_BYTES >> 4);
 #pragma unroll
                     for (int kk = 0; kk < TILE / 16; ++kk)
                         mma_ts(tmem + C::TM_O, tmem + C::TM_S + buf * TILE + kk * 8, dv + (kk * 16 * 128 >> 4),
@@ -228,132 +252,147 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 mma_commit(bar(C::BAR_DRAIN));
             __syncwarp();
             warp_wait(C::BAR_DRAIN, 0, CHUNK_ERR_DRAIN);
+        } else if (warp == C::WARP_LOAD) {
+            // ======================================== pages -> stages
+            const int box_shift = a.c.page_shift < 6 ? a.c.page_shift : 6;   // rows of a box
+            const int boxes = TILE >> box_shift;               // of a tile: one a lane
+            const uint32_t box_bytes = static_cast<uint32_t>(D) << box_shift;
+            const uint32_t offset = static_cast<uint32_t>(lane) * C::ROW << box_shift;   // in each panel
+            uint32_t issued = 0;                               // tiles
+            bool ok = true;
+            do {
+                int tile0, tile1;
+                part_of(tile0, tile1);
+                const int n = tile1 - tile0, h = line.h;
+                const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
+                const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
+                auto pos_at = [&](int j) { return from + j * TILE + (lane << box_shift); };
+                auto page_at = [&](int j) {                    // -1: none, or not seen
+                    const int pos = pos_at(j);
+                    const bool seen = j < n && lane < boxes && pos < stop && pos + (1 << box_shift) > line.span.lo;
+                    return seen ? page_of(a.c, line.b, pos >> a.c.page_shift) : -1;
+                };
+                auto scales_of = [&](int page) -> uint32_t {
+                    if (page < 0)
+                        return 0;
+                    const long long i = static_cast<long long>(page) * a.c.H + h;
+                    return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | PAGE_BIT;
+                };
+                int id = page_at(0), id_next = page_at(1);     // pages two tiles ahead, scales one
+                uint32_t sc = scales_of(id);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int id_after = page_at(j + 2);
+                    const uint32_t sc_next = scales_of(id_next);
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box_bytes;
+                    const uint32_t g = it + j, ks = g % C::KS, vs = g % C::VS;
+                    const int slot = pos_at(j) & ((1 << a.c.page_shift) - 1);
+                    if (g >= C::KS && !(ok = warp_wait(C::BAR_K_EMPTY + ks, (g / C::KS - 1) & 1, CHUNK_ERR_LOAD)))
+                        break;
+                    if (g >= C::VS && !(ok = warp_wait(C::BAR_RAW_EMPTY + vs, (g / C::VS - 1) & 1, CHUNK_ERR_LOAD)))
+                        break;
+                    // For each group of 16 keys: 2^ek, ev, 2^-ev, and the scales' word (which
+                    // tells a NaN scale).  The tile eight back is done with: its values'
+                    // stage came back twice.
+                    if (lane < boxes) {
+                        const int kb = sc & 255, vb = sc >> 8 & 255;
+                        const int ek = kb == 255 ? 0 : kb - 127, ev = vb == 255 ? 0 : vb - 127;
+                        const float4 f = make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev), __uint_as_float(sc));
+                        for (int k = 0; k < 1 << (box_shift - 4); ++k)
+                            reinterpret_cast<float4 *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES)[(lane << (box_shift - 4)) + k] = f;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(C::BAR_K_FULL + ks), bytes);
+                        mbar_arrive_expect_tx(bar(C::BAR_RAW_FULL + vs), bytes);
+                    }
+                    __syncwarp();
+                    if (id >= 0)
+#pragma unroll
+                        for (int p = 0; p < C::PANELS; ++p) {
+                            tma_load_4d(base + C::OFF_K + ks * C::STAGE + p * C::PANEL + offset, &k_map, p * 128, slot, h, id,
+                                        bar(C::BAR_K_FULL + ks));
+                            tma_load_4d(base + C::OFF_RAW + vs * C::STAGE + p * C::PANEL + offset, &v_map, p * 128, slot, h, id,
+                                        bar(C::BAR_RAW_FULL + vs));
+                        }
+                    issued = g + 1;
+                    id = id_next;
+                    id_next = id_after;
+                    sc = sc_next;
+                }
+                it += n;
+            } while (ok && next_unit());
+            // the copies in flight have landed before the CTA goes
+            for (uint32_t g = issued > C::VS ? issued - C::VS : 0; g < issued; ++g) {
+                warp_wait(C::BAR_RAW_FULL + g % C::VS, g / C::VS & 1, CHUNK_ERR_DRAIN);
+                if (g + C::KS >= issued)
+                    warp_wait(C::BAR_K_FULL + g % C::KS, g / C::KS & 1, CHUNK_ERR_DRAIN);
+            }
         }
     } else if (warp >= C::WARP_CONVERT) {
-        // ============================================ codes -> f16 operands
-        // A warp takes blocks of 8 rows by 64 bytes: rows 8 w .. and 8 (w + 4) .. of every
-        // panel, so two 16-key groups a tile.
-        constexpr int NL = D / 32;                       // 16-byte pieces a thread takes of K
-        const int w = warp - C::WARP_CONVERT, c = lane >> 3;
-        const int row0 = w * 8 + (lane & 7);             // piece i: row row0 + 32 (i & 1), panel i / 2
-        auto piece = [&](int off, uint32_t buf, int i) {
-            return base + off + buf * C::KV_BYTES + (i >> 1) * C::KV_PANEL + (row0 + 32 * (i & 1)) * 128;
+        // ============================================ values' codes -> f16 operands
+        if constexpr (C::REG_SPLIT)
+            setmaxnreg_dec<C::REG_CONVERT>();
+        // Eight lanes take eight rows of one 16-byte column: the swizzles of both sides spread
+        // them over all banks.
+        constexpr int NL = D / 32;                       // 16-byte pieces a thread takes
+        const int w = warp - C::WARP_CONVERT;
+        const int row0 = w * 8 + (lane & 7);             // piece i: row row0 + 32 (i & 1), column 4 (i / 2) + c
+        const int c = lane >> 3;
+        auto raw_at = [&](uint32_t stage, int i) {
+            const int row = row0 + 32 * (i & 1), col = (i >> 1) * 4 + c;
+            const int panel = col * 16 / C::ROW, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
+            return base + C::OFF_RAW + stage * C::STAGE + panel * C::PANEL + row * C::ROW + ((col % (C::ROW / 16) ^ x) << 4);
         };
         bool ok = true;
         do {
             int tile0, tile1;
             part_of(tile0, tile1);
-            const int n = tile1 - tile0, b = line.b, h = line.h;
+            const int n = tile1 - tile0;
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
             int all_lo, all_hi;
             line.seen_by_all(a, all_lo, all_hi);
-            // Pages and scales of 32 groups (eight tiles) at a time, one a lane, loaded one
-            // and two batches ahead.
-            auto table_batch = [&](int k) {
-                const long long pos = from + static_cast<long long>(k + lane) * CHUNK;
-                return pos < stop ? page_of(a.c, b, static_cast<int>(pos) >> a.c.page_shift) : -1;
-            };
-            auto scale_batch = [&](int id) -> uint32_t {
-                if (id < 0)
-                    return 0;
-                const long long i = static_cast<long long>(id) * a.c.H + h;
-                return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | INFO_PAGE;
-            };
-            int id_now = table_batch(0), id_next = table_batch(32), id_after = table_batch(64);
-            uint32_t sc_now = scale_batch(id_now), sc_next = scale_batch(id_next);
-
-            uint4 k_reg[NL], v_reg[NL];
-            uint32_t info = 0;                           // lane i < GROUPS: group i of the tile to come
-            int id_row[2];                               // pages of this thread's two rows
-            auto advance = [&](int j) {                  // to tile j
-                if (j > 0 && (j & 7) == 0) {
-                    id_now = id_next;
-                    id_next = id_after;
-                    sc_now = sc_next;
-                    sc_next = scale_batch(id_next);
-                    id_after = table_batch(j * GROUPS + 64);
-                }
-                info = __shfl_sync(0xffffffffu, sc_now, (j & 7) * GROUPS + (lane & (GROUPS - 1)));
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    id_row[r] = __shfl_sync(0xffffffffu, id_now, (j & 7) * GROUPS + (w >> 1) + 2 * r);
-            };
-            auto load = [&](uint4 (&reg)[NL], const Half &half, int j) {
-                const uint8_t *p[2];
-                bool seen[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int pos = from + j * TILE + row0 + 32 * r, slot = pos & ((1 << a.c.page_shift) - 1);
-                    // positions that no row of the block sees are zeros
-                    seen[r] = id_row[r] >= 0 && pos >= line.span.lo && pos < stop;
-                    p[r] = half.codes + id_row[r] * half.s_page + h * half.s_head + slot * half.s_slot + c * 16;
-                }
+            for (int j = 0; j < n; ++j) {
+                const uint32_t g = it + j, buf = g & 1, stage = g % C::VS;
+                const int pos0 = from + j * TILE;
+                if (!(ok = warp_wait(C::BAR_RAW_FULL + stage, g / C::VS & 1, CHUNK_ERR_CONVERT)))
+                    break;
+                uint4 v[NL];
 #pragma unroll
                 for (int i = 0; i < NL; ++i)
-                    reg[i] = seen[i & 1] ? __ldg(reinterpret_cast<const uint4 *>(p[i & 1] + (i >> 1) * 64)) : make_uint4(0, 0, 0, 0);
-            };
-            advance(0);
-            load(k_reg, a.c.k, 0);
-            load(v_reg, a.c.v, 0);
-            for (int j = 0; j < n && ok; ++j) {
-                const uint32_t g = it + j, buf = g & 1, par = (g >> 1 & 1) ^ 1, slot = g & 3;
-                const int pos0 = from + j * TILE;
-                if (g >= 2 && !(ok = warp_wait(C::BAR_K_EMPTY + buf, par, CHUNK_ERR_CONVERT)))
-                    break;
-                const bool pages = __all_sync(0xffffffffu, (info & INFO_PAGE) && (info & 255) != 255 && (info >> 8 & 255) != 255);
-                const bool whole = pages && pos0 >= all_lo && pos0 + TILE <= all_hi;
-                bool nan = false;
-                if (!whole) {
+                    ld_shared_v4(raw_at(stage, i), v[i].x, v[i].y, v[i].z, v[i].w);
+                if (!all_whole(smem, g, pos0, all_lo, all_hi)) {
                     // Rows of the block see different keys of this tile, and a NaN value
                     // times a weight of 0 is NaN: such values become zeros here, and their
-                    // places go to the softmax warps.
-                    uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + slot * C::NAN_BYTES);
+                    // places go to the softmax warps.  Keys that no row sees are zeros, too
+                    // (without a page, what lies in their place may be anything).
+                    uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
+                    bool nan = false;
 #pragma unroll
                     for (int i = 0; i < NL; ++i) {
-                        const int row = row0 + 32 * (i & 1);
-                        const uint32_t sc = __shfl_sync(0xffffffffu, info, row >> 4);
-                        uint32_t m = nan_bits(v_reg[i].x) | nan_bits(v_reg[i].y) << 4 | nan_bits(v_reg[i].z) << 8 |
-                                     nan_bits(v_reg[i].w) << 12;
-                        const int pos = pos0 + row;
-                        if ((sc & INFO_PAGE) && (sc >> 8 & 255) == 255 && pos >= line.span.lo && pos < stop)
-                            m = 0xffffu;   // a NaN scale
-                        if (m)
-                            v_reg[i] = make_uint4(without_nan(v_reg[i].x), without_nan(v_reg[i].y),
-                                                  without_nan(v_reg[i].z), without_nan(v_reg[i].w));
+                        const int row = row0 + 32 * (i & 1), pos = pos0 + row;
+                        const uint32_t sc = group_word(smem, g, row >> 4);
+                        const bool seen = (sc & PAGE_BIT) && pos >= line.span.lo && pos < stop;
+                        uint32_t m = nan_bits(v[i].x) | nan_bits(v[i].y) << 4 | nan_bits(v[i].z) << 8 | nan_bits(v[i].w) << 12;
+                        m = !seen ? 0 : (sc >> 8 & 255) == 255 ? 0xffffu : m;
+                        v[i] = seen ? make_uint4(without_nan(v[i].x), without_nan(v[i].y), without_nan(v[i].z), without_nan(v[i].w))
+                                    : make_uint4(0, 0, 0, 0);
                         nan |= m != 0;
                         map[row * (D / 16) + (i >> 1) * 4 + c] = static_cast<uint16_t>(m);
                     }
                     nan = __any_sync(0xffffffffu, nan);
+                    if (lane == 0)   // one byte a warp
+                        smem[C::OFF_FLAGS + (g & 3) * 4 + w] = nan;
                 }
-                uint32_t *const words = reinterpret_cast<uint32_t *>(smem + C::OFF_INFO + slot * C::INFO_BYTES);
-                if (w == 0 && lane < GROUPS) {
-                    // (a NaN scale: the softmax warps go by its byte)
-                    const int kb = info & 255, vb = info >> 8 & 255;
-                    const int ek = kb == 255 ? 0 : kb - 127, ev = vb == 255 ? 0 : vb - 127;
-                    reinterpret_cast<float4 *>(words)[lane] =
-                        make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev), __uint_as_float(info));
-                }
-                if (lane == 0)   // flags, one byte a warp
-                    reinterpret_cast<uint8_t *>(words + GROUPS * 4)[w] = (whole ? FLAG_WHOLE : 0) | (nan ? FLAG_NAN : 0);
-#pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    store_f16(piece(C::OFF_K, buf, i), row0, c * 2, k_reg[i]);
-                fence_proxy_async_shared();
-                warp_arrive(C::BAR_K_FULL + buf);
-                if (j + 1 < n) {   // the next tile's keys come in while these values are converted
-                    advance(j + 1);
-                    load(k_reg, a.c.k, j + 1);
-                }
-                if (g >= 2 && !(ok = warp_wait(C::BAR_V_EMPTY + buf, par, CHUNK_ERR_CONVERT)))
+                warp_arrive(C::BAR_RAW_EMPTY + stage);
+                if (g >= 2 && !(ok = warp_wait(C::BAR_V_EMPTY + buf, (g >> 1 & 1) ^ 1, CHUNK_ERR_CONVERT)))
                     break;
 #pragma unroll
                 for (int i = 0; i < NL; ++i)
-                    store_f16(piece(C::OFF_V, buf, i), row0, c * 2, v_reg[i]);
+                    store_f16(base + C::OFF_V + buf * C::V_BYTES + (i >> 1) * C::V_PANEL + (row0 + 32 * (i & 1)) * 128, row0, c * 2,
+                              v[i]);
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_V_FULL + buf);
-                if (j + 1 < n)
-                    load(v_reg, a.c.v, j + 1);
             }
             it += n;
         } while (ok && next_unit());
@@ -383,44 +422,53 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 const long long x = static_cast<long long>(pos) - a.window;
                 lo = x > 0 ? static_cast<int>(x) : 0;
             }
-            // ---- this row of Q, times the power of two that brings its largest
-            // magnitude to [2^14, 2^15), as f16
+            // ---- this row of Q as two e4m3 terms, times the power of two that brings its
+            // largest magnitude to [224, 448)
             int e;
             {
                 const uint16_t *q = static_cast<const uint16_t *>(a.q) + b * a.q_sb + hq * a.q_sh + tok * a.q_sl;
                 uint32_t top = 0;
-#pragma unroll
+#pragma unroll 8
                 for (int c = 0; c < D / 8; ++c) {
                     const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c) : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t u = w[k] & 0x7fffu, v = (w[k] >> 16) & 0x7fffu;
-                        top = top > u ? top : u;
-                        top = top > v ? top : v;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
                 }
-                e = static_cast<int>(top >> 7) - 127 - 14;
+                // 448 = 1.75 * 2^8
+                e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) >= 0x60u ? 1 : 0);
                 e = e < -126 ? -126 : e;
                 // a row with an infinity or NaN has no finite scores: make it NaN
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
                 if (unit > 0 && !(ok = warp_wait(C::BAR_Q_EMPTY, (unit - 1) & 1, CHUNK_ERR_SOFTMAX)))
                     break;
-#pragma unroll 8
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[4];
+#pragma unroll 2
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t t0[4], t1[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-                    st_shared_v4(base + C::OFF_Q + (c >> 3) * C::Q_PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4), y[0], y[1],
-                                 y[2], y[3]);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c * 2 + half) : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            uint32_t y0 = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+                            uint32_t y1 = pack_f16x2(__uint_as_float(w[k + 1] << 16) * f, __uint_as_float(w[k + 1] & 0xffff0000u) * f);
+                            t0[half * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                            t1[half * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                        }
+                    }
+                    const int panel = c * 16 / C::ROW, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
+                    const uint32_t at = base + C::OFF_Q + panel * C::Q_PANEL + row * C::ROW + ((c % (C::ROW / 16) ^ x) << 4);
+                    st_shared_v4(at, t0[0], t0[1], t0[2], t0[3]);
+                    st_shared_v4(at + C::Q_TERM, t1[0], t1[1], t1[2], t1[3]);
                 }
                 fence_proxy_async_shared();
                 warp_arrive(C::BAR_Q_FULL);
             }
 
+            int all_lo, all_hi;
+            line.seen_by_all(a, all_lo, all_hi);
             const float scale_row = scale_log2 * pow2i(e);
             float M = -INFINITY, l = 0.f;
             uint32_t nan[C::NAN_WORDS];   // values of O that a visible NaN value makes NaN
@@ -436,8 +484,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 uint32_t r0[32], r1[32];
                 tmem_ld32(s_addr, r0);
                 tmem_ld32(s_addr + 32, r1);
-                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES);
-                const uint32_t flags = __float_as_uint(info[GROUPS].x);
+                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES);
                 float c[GROUPS], ev[GROUPS], lf[GROUPS];      // x = S * c
 #pragma unroll
                 for (int q = 0; q < GROUPS; ++q) {
@@ -448,13 +495,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                 }
                 tmem_ld_wait(r0);
                 tmem_ld_wait(r1);
-                const bool whole = flags & FLAG_WHOLE;
-                if (!whole) {             // scores that the row does not see
-                    const int pos0 = from + j * TILE;
+                const int pos0 = from + j * TILE;
+                if (!all_whole(smem, g, pos0, all_lo, all_hi)) {   // scores that the row does not see
 #pragma unroll
                     for (int q = 0; q < GROUPS; ++q) {
                         const uint32_t word = __float_as_uint(info[q].w);
-                        const bool page = word & INFO_PAGE, nan_scale = (word & 255) == 255;
+                        const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
 #pragma unroll
                         for (int k = q * CHUNK; k < (q + 1) * CHUNK; ++k) {
                             uint32_t &x = k < 32 ? r0[k & 31] : r1[k & 31];
@@ -462,7 +508,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS) chunk_kernel(const AttnArgs a, 
                             x = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : x;
                         }
                     }
-                    if (flags & 0x02020202u) {
+                    // NaN values, once the tile's are converted
+                    if (!(ok = warp_wait(C::BAR_V_FULL + buf, g >> 1 & 1, CHUNK_ERR_SOFTMAX)))
+                        break;
+                    if (*reinterpret_cast<const uint32_t *>(smem + C::OFF_FLAGS + (g & 3) * 4)) {
                         const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
 #pragma unroll 1
                         for (int k = 0; k < TILE; ++k)
@@ -641,6 +690,12 @@ fa2_status launch_chunk(const AttnArgs &a)
     if (!parts_of<C>(a, parts))
         return FA2_ERR_INVALID_ARG;
     const int grid = line_grid<C>(a, parts.data != nullptr);
+    const EncodeTiled encode = encode_tiled();
+    CUtensorMap k_map, v_map;
+    const int rows = a.c.page_shift < 6 ? 1 << a.c.page_shift : C::TILE;
+    if (!encode || !page_map(encode, &k_map, a.c.k, a.c, C::D, rows, C::ROW) ||
+        !page_map(encode, &v_map, a.c.v, a.c, C::D, rows, C::ROW))
+        return FA2_ERR_CUDA;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
         return FA2_ERR_CUDA;
@@ -653,7 +708,7 @@ fa2_status launch_chunk(const AttnArgs &a)
         }
         configured.fetch_or(bit);
     }
-    chunk_kernel<C><<<grid, C::T, C::SMEM_BYTES, a.stream>>>(a, parts);
+    chunk_kernel<C><<<grid, C::T, C::SMEM_BYTES, a.stream>>>(k_map, v_map, a, parts);
     return cudaGetLastError() == cudaSuccess ? FA2_OK : FA2_ERR_CUDA;
 }
 #endif

@@ -34,9 +34,9 @@
 #pragma once
 
 #include <atomic>
-#include <cuda.h>
 
 #include "fa2_cache_line.cuh"
+#include "fa2_cache_tile.cuh"
 
 namespace fa2 {
 namespace cache {
@@ -84,29 +84,8 @@ struct StepCfg {
     static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && Q_PANEL % 512 == 0, "swizzle atoms");
 };
 
-// A page's scales as the loading warp hands them on: key byte, value byte, this bit (0: no page).
-constexpr uint32_t STEP_PAGE = 1u << 16;
-
 // Error codes of waits that ran out (bits 8-11 the waiting role).
 constexpr int STEP_ERR_SOFTMAX = 12 << 8, STEP_ERR_LOAD = 13 << 8, STEP_ERR_MMA = 14 << 8, STEP_ERR_DRAIN = 15 << 8;
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled();   // the driver's cuTensorMapEncodeTiled, or null
-
-// One page and head of codes: a box of page_size rows by `row` bytes, swizzled over `row`.
-inline bool page_map(EncodeTiled encode, CUtensorMap *m, const Half &x, const View &c, int D, int row)
-{
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), 1ull << c.page_shift, static_cast<cuuint64_t>(c.H),
-                                static_cast<cuuint64_t>(c.num_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.s_slot), static_cast<cuuint64_t>(x.s_head),
-                                   static_cast<cuuint64_t>(x.s_page)};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(row), 1u << c.page_shift, 1, 1}, step[4] = {1, 1, 1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, x.codes, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 #ifdef __CUDACC__
 
@@ -136,31 +115,6 @@ __device__ __forceinline__ float warp_max(float v)
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
-}
-
-// Shared-memory matrix descriptor for rows of 64 bytes swizzled over 64 (layout type 4),
-// otherwise as ptx::sdesc_sw128.
-__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo)
-{
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4 & 0x3FFFu) << 16 |
-           static_cast<uint64_t>(sbo >> 4 & 0x3FFFu) << 32 | 1ull << 46 | 4ull << 61;
-}
-
-// Takes the next e4m3 term off an f16 pair: its codes (round to nearest even, saturating),
-// and 16 times what is left, exactly: the rounding error of four bits' worth of eleven.
-__device__ __forceinline__ uint32_t take_term(uint32_t &pair)
-{
-    uint32_t codes, rest;
-    asm("{\n\t.reg .b16 c;\n\t.reg .b32 x;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 c, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 x, c;\n\t"
-        "sub.rn.f16x2 x, %2, x;\n\t"
-        "mul.rn.f16x2 %1, x, %3;\n\t"
-        "cvt.u32.u16 %0, c;\n\t}"
-        : "=r"(codes), "=r"(rest)
-        : "r"(pair), "r"(0x4c004c00u));   // 16, 16
-    pair = rest;
-    return codes;
 }
 
 template <class C>
@@ -246,7 +200,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 if (page < 0)
                     return 0;
                 const long long i = static_cast<long long>(page) * a.c.H + h;
-                return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | STEP_PAGE;
+                return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | PAGE_BIT;
             };
             int id = page_at(0), id_next = page_at(1);     // pages two tiles ahead, scales one
             uint32_t sc = scales_of(id);
@@ -415,7 +369,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const int d = d0 + 4 * k, panel = d / C::ROW, col = d % C::ROW;
 #pragma unroll
                     for (int term = 0; term < 2; ++term) {
-                        const uint32_t lo = take_term(x01), hi = take_term(x23);
+                        const uint32_t lo = take_term<16>(x01), hi = take_term<16>(x23);
                         const int row = term * R + r, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
                         *reinterpret_cast<uint32_t *>(smem + C::OFF_Q + panel * C::Q_PANEL + row * C::ROW +
                                                       (((col >> 4) ^ x) << 4) + (col & 15)) = lo | hi << 16;
@@ -557,7 +511,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         uint32_t y = pack_f16x2(y0, y1);
 #pragma unroll
                         for (int term = 0; term < 3; ++term)
-                            p[term][r / 2] = take_term(y);
+                            p[term][r / 2] = take_term<16>(y);
                     }
                 }
                 // Keys that not every row sees: what lies in their slots' place in shared memory
@@ -731,7 +685,9 @@ fa2_status launch_step(const AttnArgs &a)
     const int grid = line_grid<C>(a, parts.data != nullptr);
     const EncodeTiled encode = encode_tiled();
     CUtensorMap k_map, v_map;
-    if (!encode || !page_map(encode, &k_map, a.c.k, a.c, C::D, C::ROW) || !page_map(encode, &v_map, a.c.v, a.c, C::D, C::ROW))
+    const int rows = 1 << a.c.page_shift;
+    if (!encode || !page_map(encode, &k_map, a.c.k, a.c, C::D, rows, C::ROW) ||
+        !page_map(encode, &v_map, a.c.v, a.c, C::D, rows, C::ROW))
         return FA2_ERR_CUDA;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)

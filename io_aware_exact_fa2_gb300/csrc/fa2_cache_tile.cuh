@@ -1,0 +1,64 @@
+// fa2_cache_tile.cuh -- what the kernels that bring the cache's pages into shared memory by
+// TMA share: tensor maps, matrix descriptors, and values as sums of e4m3 terms.
+#pragma once
+
+#include <cuda.h>
+
+#include "fa2_cache.cuh"
+
+namespace fa2 {
+namespace cache {
+
+// A page's scales as a loading warp hands them on: key byte, value byte, this bit (0: no page).
+constexpr uint32_t PAGE_BIT = 1u << 16;
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled();   // the driver's cuTensorMapEncodeTiled, or null
+
+// Codes of a page and head: boxes of `rows` rows by `row` bytes, swizzled over `row`.
+inline bool page_map(EncodeTiled encode, CUtensorMap *m, const Half &x, const View &c, int D, int rows, int row)
+{
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), 1ull << c.page_shift, static_cast<cuuint64_t>(c.H),
+                                static_cast<cuuint64_t>(c.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.s_slot), static_cast<cuuint64_t>(x.s_head),
+                                   static_cast<cuuint64_t>(x.s_page)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(row), static_cast<cuuint32_t>(rows), 1, 1}, step[4] = {1, 1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, x.codes, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+#ifdef __CUDACC__
+// Shared-memory matrix descriptor for rows of 64 bytes swizzled over 64 (layout type 4),
+// otherwise as ptx::sdesc_sw128.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4 & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(sbo >> 4 & 0x3FFFu) << 32 | 1ull << 46 | 4ull << 61;
+}
+
+// Takes the next e4m3 term off an f16 pair: its codes (round to nearest even, saturating),
+// and SCALE (16 or 1) times what is left, exactly: the rounding error of four bits' worth of
+// eleven.
+template <int SCALE>
+__device__ __forceinline__ uint32_t take_term(uint32_t &pair)
+{
+    uint32_t codes, rest;
+    asm("{\n\t.reg .b16 c;\n\t.reg .b32 x;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 c, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 x, c;\n\t"
+        "sub.rn.f16x2 x, %2, x;\n\t"
+        "mul.rn.f16x2 %1, x, %3;\n\t"
+        "cvt.u32.u16 %0, c;\n\t}"
+        : "=r"(codes), "=r"(rest)
+        : "r"(pair), "r"(SCALE == 16 ? 0x4c004c00u : 0x3c003c00u));   // SCALE, SCALE
+    pair = rest;
+    return codes;
+}
+
+#endif
+
+}  // namespace cache
+}  // namespace fa2
