@@ -3,7 +3,8 @@
 //
 // A unit is a block of C::R query rows of one (sequence, key/value head); it spans the
 // tiles of C::TILE keys that any of its rows sees.  Units lie on the line in the order
-// sequence, head, row block, so that CTAs that run side by side read the same keys.
+// sequence, row block, head: the heads of a row block are alike, so a place on the line is
+// found among the row blocks, which the threads of a CTA share out.
 // A unit is C::UNIT_COST tiles longer on the line than it is, for what it costs to begin and
 // end one; a range that holds only of those has nothing to do with the unit.
 // Lengths are device data, so every CTA lays out the line for itself.
@@ -130,19 +131,6 @@ struct Range {
     __device__ int owner(long long x) const { return static_cast<int>(divide((x + 1) * grid + total - 1, total) - 1); }
 };
 
-// Length on the line of one head's units of a sequence.
-template <class C>
-__device__ __forceinline__ long long tiles_of(const AttnArgs &a, const Seq &s)
-{
-    const int blocks = row_blocks<C>(a, s);
-    if (!a.causal)   // every block sees all keys
-        return blocks ? static_cast<long long>(blocks) * (span_of<C>(a, s, 0).tiles + C::UNIT_COST) : 0;
-    long long n = 0;
-    for (int rb = 0; rb < blocks; ++rb)
-        n += span_of<C>(a, s, rb).tiles + C::UNIT_COST;
-    return n;
-}
-
 // A unit's place on the line.
 template <class C>
 struct Line {
@@ -154,16 +142,16 @@ struct Line {
     __device__ __forceinline__ bool next(const AttnArgs &a)   // the following unit; false at the line's end
     {
         at += span.tiles + C::UNIT_COST;
+        if (++h < a.c.H)
+            return true;
+        h = 0;
         if (++rb == row_blocks<C>(a, s)) {
             rb = 0;
-            if (++h == a.c.H) {
-                h = 0;
-                do {
-                    if (++b == a.c.B)
-                        return false;
-                    s = sequence(a, b);
-                } while (s.n == 0);
-            }
+            do {
+                if (++b == a.c.B)
+                    return false;
+                s = sequence(a, b);
+            } while (s.n == 0);
         }
         span = span_of<C>(a, s, rb);
         return true;
@@ -181,8 +169,8 @@ struct Line {
 };
 
 struct LineShared {
-    long long scan[32], off, per_head;
-    int b, kv, n;
+    long long scan[32], at;
+    int b, rb, kv, n;
 };
 
 // Lays out the line and finds this CTA's range of it, [first, end), and the unit it
@@ -193,21 +181,34 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
                                            long long &end, Line<C> &line)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // a thread sums a run of sequences; the one whose run holds the first tile finds
-    // the sequence
-    const int per = (a.c.B + C::T - 1) / C::T;
-    const int b0 = tid * per, b1 = b0 + per < a.c.B ? b0 + per : a.c.B;
-    long long mine = 0, mine_first = 0;
-    Seq seq_first{0, 0};
-    for (int b = b0; b < b1; ++b) {
-        const Seq s = sequence(a, b);
-        const long long n = tiles_of<C>(a, s);
-        if (b == b0) {
-            seq_first = s;
-            mine_first = n;
+    // A thread takes a run of the row blocks (as many a sequence as Lq can have), and the
+    // one whose run holds the first tile finds its unit.
+    const int blocks = static_cast<int>((static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R);
+    const long long items = static_cast<long long>(a.c.B) * blocks;
+    const int per = static_cast<int>(divide(items + C::T - 1, C::T));
+    const long long i0 = static_cast<long long>(tid) * per, i1 = i0 + per < items ? i0 + per : items;
+    const int b0 = blocks == 1 ? static_cast<int>(i0) : static_cast<int>(divide(i0, blocks));
+    const int rb0 = static_cast<int>(i0 - static_cast<long long>(b0) * blocks);
+    // calls f(b, rb, sequence, the heads' length) for each of them until it returns true
+    auto walk = [&](auto f) {
+        int b = b0, rb = rb0;
+        Seq s{0, 0};
+        if (i0 < i1)
+            s = sequence(a, b);
+        for (long long i = i0; i < i1; ++i) {
+            if (rb * C::R < s.n * a.G && f(b, rb, s, (span_of<C>(a, s, rb).tiles + C::UNIT_COST) * static_cast<long long>(a.c.H)))
+                return;
+            if (++rb == blocks && i + 1 < i1) {
+                rb = 0;
+                s = sequence(a, ++b);
+            }
         }
-        mine += n * a.c.H;
-    }
+    };
+    long long mine = 0;
+    walk([&](int, int, const Seq &, long long n) {
+        mine += n;
+        return false;
+    });
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -237,33 +238,30 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     if (first >= end)
         return false;
     if (first >= before && first < before + mine) {
-        long long at = before, n = mine_first;
-        int b = b0;
-        Seq s = seq_first;
-        while (first >= at + n * a.c.H) {
-            at += n * a.c.H;
-            s = sequence(a, ++b);
-            n = tiles_of<C>(a, s);
-        }
-        sh.b = b;
-        sh.off = at;
-        sh.per_head = n;
-        sh.kv = s.kv;
-        sh.n = s.n;
+        long long at = before;
+        walk([&](int b, int rb, const Seq &s, long long n) {
+            if (first >= at + n) {
+                at += n;
+                return false;
+            }
+            sh.at = at;
+            sh.b = b;
+            sh.rb = rb;
+            sh.kv = s.kv;
+            sh.n = s.n;
+            return true;
+        });
     }
     __syncthreads();
     line.b = sh.b;
-    line.at = sh.off;
+    line.rb = sh.rb;
     line.s = Seq{sh.kv, sh.n};
-    const long long per_head = sh.per_head;
-    line.h = static_cast<int>(divide(first - line.at, per_head));
-    line.rb = 0;
-    line.at += line.h * per_head;
-    line.span = span_of<C>(a, line.s, 0);
-    while (line.at + line.span.tiles <= first)   // (next() may end past `first`, in a unit's extra length)
-        if (!line.next(a))
-            return false;
-    if (!cut && line.at < first && !line.next(a))
+    line.span = span_of<C>(a, line.s, line.rb);
+    const int length = line.span.tiles + C::UNIT_COST;
+    line.h = static_cast<int>(divide(first - sh.at, length));
+    line.at = sh.at + static_cast<long long>(line.h) * length;
+    // (the range may begin in a unit's extra length: then with the next unit)
+    if ((line.at + line.span.tiles <= first || (!cut && line.at < first)) && !line.next(a))
         return false;
     return line.at < end;
 }
