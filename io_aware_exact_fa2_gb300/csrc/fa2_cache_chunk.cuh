@@ -9,11 +9,12 @@
 // exact but for elements below 2^-9 of their row's largest, which are off by up to 2^-17 of
 // that.  For key j of a page with exponents ek, ev
 //     x_j = S_j * scale * log2 e * 2^(e + ek),   p'_j = 2^(x_j + ev - M + 6)
-//     O += P' V,   l += 2^-ev sum p'             M: running maximum of x + ev
+//     O += P' V,   l += 2^-ev sum p'             M: a maximum of x + ev so far
 // so both exponents ride in the one multiply-add before the exponential, at no cost, and one
 // accumulator takes pages of any strength.  P' is f16 (two terms of e4m3 would not span a
-// long context's weights) and V is converted to f16, exactly.  M is raised only when a tile
-// exceeds it by more than 2^8: p' stays within 2^14.
+// long context's weights) and V is converted to f16, exactly.  M is raised only when the
+// weights that a tile has by it would leave f16's range, which their sum tells: most tiles
+// need no maximum at all.
 //
 // What bounds it.  4 D operations a (row, key) pair against D / 64 cache bytes a row and
 // key: the tensor pipe.  (Two e4m3 products take the time of one of f16, and K needs no
@@ -49,7 +50,7 @@ struct ChunkCfg {
     // With two CTAs an SM the launch leaves 80 registers a thread, 240 for the three
     // warpgroups' lanes together: the softmax rises, the others give.
     static constexpr bool REG_SPLIT = CTAS == 2;
-    static constexpr int REG_SOFTMAX = 128, REG_CONVERT = 64, REG_ISSUE = 48;
+    static constexpr int REG_SOFTMAX = 144, REG_CONVERT = 56, REG_ISSUE = 40;
     static_assert(REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 3 * 80, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
@@ -61,7 +62,7 @@ struct ChunkCfg {
     static constexpr int OFF_Q = 0, OFF_V = 2 * Q_TERM, OFF_K = OFF_V + 2 * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
     // a ring of eight tiles' group scales; of four tiles' NaN flags and NaN values by key
     static constexpr int NAN_WORDS = D / 32;
-    static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16;
+    static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16;
     static constexpr int OFF_FLAGS = OFF_INFO + 8 * INFO_BYTES;
     static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
     static constexpr int OFF_BAR = OFF_NAN + 4 * NAN_BYTES;
@@ -160,18 +161,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         tile1 = cut && end < line.at + line.span.tiles ? static_cast<int>(end - line.at) : line.span.tiles;
     };
     auto next_unit = [&]() { return line.next(a) && line.at < end; };
-    // a group's scales (see the loading warp); whether every row sees every key of tile g
+    // what the loading warp says of tile g: a group's scales, and whether every row sees every key
     auto group_word = [](const uint8_t *smem, uint32_t g, int q) {
         return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES)[q * 4 + 3];
     };
-    auto all_whole = [&](const uint8_t *smem, uint32_t g, int pos0, int all_lo, int all_hi) {
-        bool whole = pos0 >= all_lo && pos0 + TILE <= all_hi;
-#pragma unroll
-        for (int q = 0; q < GROUPS; ++q) {
-            const uint32_t sc = group_word(smem, g, q);
-            whole &= (sc & PAGE_BIT) && (sc & 255) != 255 && (sc >> 8 & 255) != 255;
-        }
-        return whole;
+    auto is_whole = [](const uint8_t *smem, uint32_t g) {
+        return *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES + GROUPS * 16) != 0;
     };
     uint32_t it = 0;       // tiles before the present unit's first: buffers alternate by tile
     uint32_t unit = 0;
@@ -278,6 +273,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const long long i = static_cast<long long>(page) * a.c.H + h;
                     return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | PAGE_BIT;
                 };
+                int all_lo, all_hi;
+                line.seen_by_all(a, all_lo, all_hi);
                 int id = page_at(0), id_next = page_at(1);     // pages two tiles ahead, scales one
                 uint32_t sc = scales_of(id);
                 for (int j = 0; j < n && ok; ++j) {
@@ -291,8 +288,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     if (g >= C::VS && !(ok = warp_wait(C::BAR_RAW_EMPTY + vs, (g / C::VS - 1) & 1, CHUNK_ERR_LOAD)))
                         break;
                     // For each group of 16 keys: 2^ek, ev, 2^-ev, and the scales' word (which
-                    // tells a NaN scale).  The tile eight back is done with: its values'
-                    // stage came back twice.
+                    // tells a NaN scale); and whether every row sees every key of the tile.
+                    // The tile eight back is done with: its values' stage came back twice.
+                    const int pos0 = from + j * TILE;
+                    const bool fine = lane >= boxes || ((sc & PAGE_BIT) && (sc & 255) != 255 && (sc >> 8 & 255) != 255);
+                    const bool whole = __all_sync(0xffffffffu, fine) && pos0 >= all_lo && pos0 + TILE <= all_hi;
+                    if (lane == 0)
+                        *reinterpret_cast<uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES + GROUPS * 16) = whole;
                     if (lane < boxes) {
                         const int kb = sc & 255, vb = sc >> 8 & 255;
                         const int ek = kb == 255 ? 0 : kb - 127, ev = vb == 255 ? 0 : vb - 127;
@@ -350,8 +352,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             const int n = tile1 - tile0;
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
-            int all_lo, all_hi;
-            line.seen_by_all(a, all_lo, all_hi);
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = it + j, buf = g & 1, stage = g % C::VS;
                 const int pos0 = from + j * TILE;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 #pragma unroll
                 for (int i = 0; i < NL; ++i)
                     ld_shared_v4(raw_at(stage, i), v[i].x, v[i].y, v[i].z, v[i].w);
-                if (!all_whole(smem, g, pos0, all_lo, all_hi)) {
+                if (!is_whole(smem, g)) {
                     // Rows of the block see different keys of this tile, and a NaN value
                     // times a weight of 0 is NaN: such values become zeros here, and their
                     // places go to the softmax warps.  Keys that no row sees are zeros, too
@@ -467,8 +467,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 warp_arrive(C::BAR_Q_FULL);
             }
 
-            int all_lo, all_hi;
-            line.seen_by_all(a, all_lo, all_hi);
             const float scale_row = scale_log2 * pow2i(e);
             float M = -INFINITY, l = 0.f;
             uint32_t nan[C::NAN_WORDS];   // values of O that a visible NaN value makes NaN
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 tmem_ld_wait(r0);
                 tmem_ld_wait(r1);
                 const int pos0 = from + j * TILE;
-                if (!all_whole(smem, g, pos0, all_lo, all_hi)) {   // scores that the row does not see
+                if (!is_whole(smem, g)) {   // scores that the row does not see
 #pragma unroll
                     for (int q = 0; q < GROUPS; ++q) {
                         const uint32_t word = __float_as_uint(info[q].w);
@@ -521,56 +519,55 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                                     nan[q] |= map[k * C::NAN_WORDS + q];
                     }
                 }
-                // running maximum of x + ev
-                float top = -INFINITY;
+                // Weights as f16 pairs, by the maximum so far.  Their sum tells whether one is
+                // too large for it: only then (and for a row's first keys) is the tile's maximum
+                // taken, O and l brought to it, and the weights taken again.
+                uint32_t p[32];
+                float sums[GROUPS];
+                bool waited = j == 0;
+                bool again = M == -INFINITY && lo < pos0 + TILE && hi > pos0;
+                for (;;) {
+                    if (__any_sync(0xffffffffu, again)) {
+                        float top = -INFINITY;   // of x + ev
 #pragma unroll
-                for (int q = 0; q < GROUPS; ++q) {
-                    const uint32_t *r = q < 2 ? r0 + q * CHUNK : r1 + (q - 2) * CHUNK;
-                    float t = __uint_as_float(r[0]);
+                        for (int q = 0; q < GROUPS; ++q) {
+                            const uint32_t *r = q < 2 ? r0 + q * CHUNK : r1 + (q - 2) * CHUNK;
+                            float t = __uint_as_float(r[0]);
 #pragma unroll
-                    for (int k = 1; k < 15; k += 2)
-                        t = max3(t, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-                    t = fmaxf(t, __uint_as_float(r[15]));
-                    top = fmaxf(top, fmaf(t, c[q], ev[q]));
-                }
-                const bool raise = top > M + 8.f, any = __any_sync(0xffffffffu, raise);
-                float f = 1.f;
-                if (raise) {
-                    f = ex2_approx(M - top);
-                    M = top;
-                    l *= f;
-                }
-                // A parity tells a phase from the one before only, so the wait below for the
-                // last tile's product needs this one taken for the last but one's, before
-                // the last can complete.
-                if (j > 0 && (any || j == n - 1)) {
-                    if (!(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
-                        break;
-                    tc_fence_after();
-                    if (any) {            // O in tensor memory stands for the old maximum
+                            for (int k = 1; k < 15; k += 2)
+                                t = max3(t, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                            t = fmaxf(t, __uint_as_float(r[15]));
+                            top = fmaxf(top, fmaf(t, c[q], ev[q]));
+                        }
+                        float f = 1.f;
+                        if (top > M) {
+                            f = ex2_approx(M - top);
+                            M = top;
+                            l *= f;
+                        }
+                        if (j > 0) {             // O in tensor memory stands for the old maximum
+                            if (!waited && !(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
+                                break;
+                            waited = true;
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            uint32_t o[32];
-                            tmem_ld32(o_addr + 32 * cc, o);
-                            tmem_ld_wait(o);
+                            for (int cc = 0; cc < D / 32; ++cc) {
+                                uint32_t o[32];
+                                tmem_ld32(o_addr + 32 * cc, o);
+                                tmem_ld_wait(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st32(o_addr + 32 * cc, o);
+                                for (int k = 0; k < 32; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st32(o_addr + 32 * cc, o);
+                            }
                         }
                     }
-                }
-                // weights, over the first half of this S buffer as f16 pairs
-                const float ref = M == -INFINITY ? 0.f : M;
+                    const float ref = 6.f - (M == -INFINITY ? 0.f : M);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int q = 0; q < GROUPS / 2; ++q) {
-                        const uint32_t *r = (half ? r1 : r0) + q * CHUNK;
-                        const int grp = half * 2 + q;
-                        const float add = ev[grp] + 6.f - ref;
-                        const uint64_t c2 = f32x2(c[grp], c[grp]), add2 = f32x2(add, add);
+                    for (int q = 0; q < GROUPS; ++q) {
+                        const uint32_t *r = q < 2 ? r0 + q * CHUNK : r1 + (q - 2) * CHUNK;
+                        const float add = ev[q] + ref;
+                        const uint64_t c2 = f32x2(c[q], c[q]), add2 = f32x2(add, add);
                         uint64_t sum2 = 0;
 #pragma unroll
                         for (int k = 0; k < CHUNK; k += 2) {
@@ -583,10 +580,23 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         }
                         float sum0, sum1;
                         unpack_f32x2(sum2, sum0, sum1);
-                        l = fmaf(sum0 + sum1, lf[grp], l);
+                        sums[q] = sum0 + sum1;
                     }
-                    tmem_st16(s_addr + half * 16, p);
+                    again = (sums[0] + sums[1]) + (sums[2] + sums[3]) > 32768.f;   // f16 ends at 65504
+                    if (!__any_sync(0xffffffffu, again))
+                        break;
                 }
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int q = 0; q < GROUPS; ++q)
+                    l = fmaf(sums[q], lf[q], l);
+                // A parity tells a phase from the one before only, so the wait for the last
+                // tile's product (below) needs that for the last but one's, before the last can
+                // complete.
+                if (!waited && j == n - 1 && !(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
+                    break;
+                tmem_st32(s_addr, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(C::BAR_P_FULL + buf);
