@@ -50,7 +50,7 @@ struct ChunkCfg {
     // With two CTAs an SM the launch leaves 80 registers a thread, 240 for the three
     // warpgroups' lanes together: the softmax rises, the others give.
     static constexpr bool REG_SPLIT = CTAS == 2;
-    static constexpr int REG_SOFTMAX = 144, REG_CONVERT = 56, REG_ISSUE = 40;
+    static constexpr int REG_SOFTMAX = 128, REG_CONVERT = 48, REG_ISSUE = 64;
     static_assert(REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 3 * 80, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
@@ -65,7 +65,8 @@ struct ChunkCfg {
     static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16;
     static constexpr int OFF_FLAGS = OFF_INFO + 8 * INFO_BYTES;
     static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
-    static constexpr int OFF_BAR = OFF_NAN + 4 * NAN_BYTES;
+    static constexpr int OFF_MARK = OFF_NAN + 4 * NAN_BYTES;         // values of O that are NaN, by row
+    static constexpr int OFF_BAR = OFF_MARK + R * NAN_WORDS * 4;
     static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_V_FULL = 2, BAR_V_EMPTY = 4, BAR_S_FULL = 6, BAR_P_FULL = 8,
                          BAR_O_DONE = 10, BAR_O_FREE = 11, BAR_GROUP = 12, BAR_DRAIN = 13, BAR_K_FULL = 14,
                          BAR_K_EMPTY = BAR_K_FULL + KS, BAR_RAW_FULL = BAR_K_EMPTY + KS, BAR_RAW_EMPTY = BAR_RAW_FULL + VS,
@@ -116,15 +117,32 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     constexpr int D = C::D, R = C::R, TILE = C::TILE, GROUPS = C::GROUPS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ LineShared sh_line;
+    // Each warp's place on the line: it changes with the unit only, and would cost the roles
+    // registers in their loops over tiles.
+    __shared__ struct {
+        Range range;
+        long long first, end;
+        Line<C> line[C::T / 32];
+    } sh;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool cut = parts.data != nullptr;
     const int cta = blockIdx.x;
-    Range range;
-    long long first, end;
-    Line<C> line;
-    if (!find_range<C>(a, cut, sh_line, range, first, end, line))
-        return;
+    {
+        Range range;
+        long long first, end;
+        Line<C> line;
+        if (!find_range<C>(a, cut, sh_line, range, first, end, line))
+            return;
+        if (lane == 0)
+            sh.line[warp] = line;
+        if (tid == 0) {
+            sh.range = range;
+            sh.first = first;
+            sh.end = end;
+        }
+    }
+    const Line<C> &line = sh.line[warp];
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *const smem = smem_raw + (base - smem_u32(smem_raw));
@@ -157,10 +175,16 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     };
     // the tiles of the unit `line` that lie in this CTA's range
     auto part_of = [&](int &tile0, int &tile1) {
-        tile0 = cut && first > line.at ? static_cast<int>(first - line.at) : 0;
-        tile1 = cut && end < line.at + line.span.tiles ? static_cast<int>(end - line.at) : line.span.tiles;
+        tile0 = cut && sh.first > line.at ? static_cast<int>(sh.first - line.at) : 0;
+        tile1 = cut && sh.end < line.at + line.span.tiles ? static_cast<int>(sh.end - line.at) : line.span.tiles;
     };
-    auto next_unit = [&]() { return line.next(a) && line.at < end; };
+    auto next_unit = [&]() -> bool {     // by a whole warp
+        __syncwarp();
+        bool more = false;
+        if (lane == 0)
+            more = sh.line[warp].next(a) && sh.line[warp].at < sh.end;
+        return __shfl_sync(0xffffffffu, more, 0);
+    };
     // what the loading warp says of tile g: a group's scales, and whether every row sees every key
     auto group_word = [](const uint8_t *smem, uint32_t g, int q) {
         return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES)[q * 4 + 3];
@@ -250,9 +274,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         } else if (warp == C::WARP_LOAD) {
             // ======================================== pages -> stages
             const int box_shift = a.c.page_shift < 6 ? a.c.page_shift : 6;   // rows of a box
-            const int boxes = TILE >> box_shift;               // of a tile: one a lane
+            const int boxes_shift = 6 - box_shift;             // boxes of a tile
             const uint32_t box_bytes = static_cast<uint32_t>(D) << box_shift;
-            const uint32_t offset = static_cast<uint32_t>(lane) * C::ROW << box_shift;   // in each panel
+            const int in_tile = lane & ((1 << boxes_shift) - 1);
+            const uint32_t offset = static_cast<uint32_t>(in_tile) * C::ROW << box_shift;   // in each panel
+            const int batch_tiles = 32 >> boxes_shift;
             uint32_t issued = 0;                               // tiles
             bool ok = true;
             do {
@@ -261,54 +287,67 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const int n = tile1 - tile0, h = line.h;
                 const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
                 const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
-                auto pos_at = [&](int j) { return from + j * TILE + (lane << box_shift); };
-                auto page_at = [&](int j) {                    // -1: none, or not seen
-                    const int pos = pos_at(j);
-                    const bool seen = j < n && lane < boxes && pos < stop && pos + (1 << box_shift) > line.span.lo;
-                    return seen ? page_of(a.c, line.b, pos >> a.c.page_shift) : -1;
+                int all_lo, all_hi;
+                line.seen_by_all(a, all_lo, all_hi);
+                // A lane has one of 32 boxes, those of the next 8 to 32 tiles: the table's
+                // entries come two such batches ahead, their scales one.
+                auto pos_at = [&](int tile) { return from + tile * TILE + (lane << box_shift); };
+                auto pages = [&](int tile) {                   // -1: none, or not seen
+                    if (tile >= n)
+                        return -1;
+                    const int pos = pos_at(tile);
+                    return pos < stop && pos + (1 << box_shift) > line.span.lo ? page_of(a.c, line.b, pos >> a.c.page_shift) : -1;
                 };
-                auto scales_of = [&](int page) -> uint32_t {
+                auto scales = [&](int page) -> uint32_t {
                     if (page < 0)
                         return 0;
                     const long long i = static_cast<long long>(page) * a.c.H + h;
                     return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | PAGE_BIT;
                 };
-                int all_lo, all_hi;
-                line.seen_by_all(a, all_lo, all_hi);
-                int id = page_at(0), id_next = page_at(1);     // pages two tiles ahead, scales one
-                uint32_t sc = scales_of(id);
-                for (int j = 0; j < n && ok; ++j) {
-                    const int id_after = page_at(j + 2);
-                    const uint32_t sc_next = scales_of(id_next);
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box_bytes;
-                    const uint32_t g = it + j, ks = g % C::KS, vs = g % C::VS;
-                    const int slot = pos_at(j) & ((1 << a.c.page_shift) - 1);
-                    if (g >= C::KS && !(ok = warp_wait(C::BAR_K_EMPTY + ks, (g / C::KS - 1) & 1, CHUNK_ERR_LOAD)))
-                        break;
-                    if (g >= C::VS && !(ok = warp_wait(C::BAR_RAW_EMPTY + vs, (g / C::VS - 1) & 1, CHUNK_ERR_LOAD)))
-                        break;
-                    // For each group of 16 keys: 2^ek, ev, 2^-ev, and the scales' word (which
-                    // tells a NaN scale); and whether every row sees every key of the tile.
-                    // The tile eight back is done with: its values' stage came back twice.
-                    const int pos0 = from + j * TILE;
-                    const bool fine = lane >= boxes || ((sc & PAGE_BIT) && (sc & 255) != 255 && (sc >> 8 & 255) != 255);
-                    const bool whole = __all_sync(0xffffffffu, fine) && pos0 >= all_lo && pos0 + TILE <= all_hi;
-                    if (lane == 0)
-                        *reinterpret_cast<uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES + GROUPS * 16) = whole;
-                    if (lane < boxes) {
+                int id = pages(0), id_next = pages(batch_tiles), id_after = pages(2 * batch_tiles), slot = 0;
+                uint32_t sc = scales(id), sc_next = scales(id_next);
+                float4 info = make_float4(0.f, 0.f, 0.f, 0.f);
+                bool fine = false;
+                for (int j = 0; j < n; ++j) {
+                    const int jj = j & (batch_tiles - 1);
+                    if (jj == 0) {
+                        if (j > 0) {
+                            id = id_next;
+                            sc = sc_next;
+                            id_next = id_after;
+                            sc_next = scales(id_next);
+                            id_after = pages(j + 2 * batch_tiles);
+                        }
+                        slot = pos_at(j) & ((1 << a.c.page_shift) - 1);
+                        // for the box's groups of 16 keys: 2^ek, ev, 2^-ev, and the scales' word
+                        // (which tells a NaN scale)
                         const int kb = sc & 255, vb = sc >> 8 & 255;
                         const int ek = kb == 255 ? 0 : kb - 127, ev = vb == 255 ? 0 : vb - 127;
-                        const float4 f = make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev), __uint_as_float(sc));
-                        for (int k = 0; k < 1 << (box_shift - 4); ++k)
-                            reinterpret_cast<float4 *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES)[(lane << (box_shift - 4)) + k] = f;
+                        info = make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev), __uint_as_float(sc));
+                        fine = (sc & PAGE_BIT) && kb != 255 && vb != 255;
                     }
+                    const bool mine = lane >> boxes_shift == jj;
+                    const uint32_t g = it + j, ks = g % C::KS, vs = g % C::VS;
+                    if ((g >= C::KS && !(ok = warp_wait(C::BAR_K_EMPTY + ks, (g / C::KS - 1) & 1, CHUNK_ERR_LOAD))) ||
+                        (g >= C::VS && !(ok = warp_wait(C::BAR_RAW_EMPTY + vs, (g / C::VS - 1) & 1, CHUNK_ERR_LOAD))))
+                        break;
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * box_bytes;
+                    const int pos0 = from + j * TILE;
+                    const bool whole = __all_sync(0xffffffffu, !mine || fine) && pos0 >= all_lo && pos0 + TILE <= all_hi;
+                    // (the tile eight back is done with: its values' stage came back twice)
+                    uint8_t *const to = smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES;
+                    if (mine)
+                        for (int k = 0; k < 1 << (box_shift - 4); ++k)
+                            reinterpret_cast<float4 *>(to)[(in_tile << (box_shift - 4)) + k] = info;
+                    if (lane == 0)               // whether every row sees every key of the tile
+                        *reinterpret_cast<uint32_t *>(to + GROUPS * 16) = whole;
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(C::BAR_K_FULL + ks), bytes);
                         mbar_arrive_expect_tx(bar(C::BAR_RAW_FULL + vs), bytes);
                     }
                     __syncwarp();
-                    if (id >= 0)
+                    if (mine && id >= 0)
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p) {
                             tma_load_4d(base + C::OFF_K + ks * C::STAGE + p * C::PANEL + offset, &k_map, p * 128, slot, h, id,
@@ -316,10 +355,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             tma_load_4d(base + C::OFF_RAW + vs * C::STAGE + p * C::PANEL + offset, &v_map, p * 128, slot, h, id,
                                         bar(C::BAR_RAW_FULL + vs));
                         }
+                    __syncwarp();
                     issued = g + 1;
-                    id = id_next;
-                    id_next = id_after;
-                    sc = sc_next;
                 }
                 it += n;
             } while (ok && next_unit());
@@ -469,44 +506,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 
             const float scale_row = scale_log2 * pow2i(e);
             float M = -INFINITY, l = 0.f;
-            uint32_t nan[C::NAN_WORDS];   // values of O that a visible NaN value makes NaN
+            // values of O that a visible NaN value makes NaN (this thread's alone)
+            uint32_t *const mark = reinterpret_cast<uint32_t *>(smem + C::OFF_MARK) + row;   // word q: [q * R]
 #pragma unroll
-            for (int k = 0; k < C::NAN_WORDS; ++k)
-                nan[k] = 0;
+            for (int q = 0; q < C::NAN_WORDS; ++q)
+                mark[q * R] = 0;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = it + j, buf = g & 1;
                 if (!(ok = warp_wait(C::BAR_S_FULL + buf, g >> 1 & 1, CHUNK_ERR_SOFTMAX)))
                     break;
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lanes + C::TM_S + buf * TILE;
-                uint32_t r0[32], r1[32];
-                tmem_ld32(s_addr, r0);
-                tmem_ld32(s_addr + 32, r1);
                 const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES);
-                float c[GROUPS], ev[GROUPS], lf[GROUPS];      // x = S * c
-#pragma unroll
-                for (int q = 0; q < GROUPS; ++q) {
-                    const float4 f = info[q];
-                    c[q] = fmaxf(scale_row * f.x, 1.17549435e-38f);   // (not 0: a hidden score is -inf * c)
-                    ev[q] = f.y;
-                    lf[q] = f.z;
-                }
-                tmem_ld_wait(r0);
-                tmem_ld_wait(r1);
                 const int pos0 = from + j * TILE;
-                if (!is_whole(smem, g)) {   // scores that the row does not see
-#pragma unroll
-                    for (int q = 0; q < GROUPS; ++q) {
-                        const uint32_t word = __float_as_uint(info[q].w);
-                        const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
-#pragma unroll
-                        for (int k = q * CHUNK; k < (q + 1) * CHUNK; ++k) {
-                            uint32_t &x = k < 32 ? r0[k & 31] : r1[k & 31];
-                            const bool see = page && pos0 + k >= lo && pos0 + k < hi;
-                            x = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : x;
-                        }
-                    }
-                    // NaN values, once the tile's are converted
+                const bool whole = is_whole(smem, g);
+                if (!whole) {            // NaN values, once the tile's are converted
                     if (!(ok = warp_wait(C::BAR_V_FULL + buf, g >> 1 & 1, CHUNK_ERR_SOFTMAX)))
                         break;
                     if (*reinterpret_cast<const uint32_t *>(smem + C::OFF_FLAGS + (g & 3) * 4)) {
@@ -516,29 +530,53 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             if (pos0 + k >= lo && pos0 + k < hi)
 #pragma unroll
                                 for (int q = 0; q < C::NAN_WORDS; ++q)
-                                    nan[q] |= map[k * C::NAN_WORDS + q];
+                                    mark[q * R] |= map[k * C::NAN_WORDS + q];
                     }
                 }
                 // Weights as f16 pairs, by the maximum so far.  Their sum tells whether one is
                 // too large for it: only then (and for a row's first keys) is the tile's maximum
                 // taken, O and l brought to it, and the weights taken again.
                 uint32_t p[32];
-                float sums[GROUPS];
+                float sum, add_l;
                 bool waited = j == 0;
                 bool again = M == -INFINITY && lo < pos0 + TILE && hi > pos0;
+                // A group of 16 scores at a time, the next one on its way from tensor memory; those
+                // that the row does not see are -inf.
+                auto for_groups = [&](auto f) {
+                    uint32_t r[2][CHUNK];
+                    tmem_ld(s_addr, r[0]);
+#pragma unroll
+                    for (int q = 0; q < GROUPS; ++q) {
+                        tmem_wait_ld();
+                        tmem_pin(r[q & 1]);
+                        if (q + 1 < GROUPS)
+                            tmem_ld(s_addr + (q + 1) * CHUNK, r[(q + 1) & 1]);
+                        if (!whole) {
+                            const uint32_t word = __float_as_uint(info[q].w);
+                            const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
+#pragma unroll
+                            for (int k = 0; k < CHUNK; ++k) {
+                                const int key = pos0 + q * CHUNK + k;
+                                const bool see = page && key >= lo && key < hi;
+                                r[q & 1][k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[q & 1][k];
+                            }
+                        }
+                        const float4 scales = info[q];
+                        // (not 0: a hidden score is -inf * c)
+                        f(q, r[q & 1], fmaxf(scale_row * scales.x, 1.17549435e-38f), scales.y, scales.z);
+                    }
+                };
                 for (;;) {
                     if (__any_sync(0xffffffffu, again)) {
                         float top = -INFINITY;   // of x + ev
-#pragma unroll
-                        for (int q = 0; q < GROUPS; ++q) {
-                            const uint32_t *r = q < 2 ? r0 + q * CHUNK : r1 + (q - 2) * CHUNK;
+                        for_groups([&](int, const uint32_t (&r)[CHUNK], float c, float ev, float) {
                             float t = __uint_as_float(r[0]);
 #pragma unroll
-                            for (int k = 1; k < 15; k += 2)
+                            for (int k = 1; k < CHUNK - 1; k += 2)
                                 t = max3(t, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-                            t = fmaxf(t, __uint_as_float(r[15]));
-                            top = fmaxf(top, fmaf(t, c[q], ev[q]));
-                        }
+                            t = fmaxf(t, __uint_as_float(r[CHUNK - 1]));
+                            top = fmaxf(top, fmaf(t, c, ev));
+                        });
                         float f = 1.f;
                         if (top > M) {
                             f = ex2_approx(M - top);
@@ -563,11 +601,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         }
                     }
                     const float ref = 6.f - (M == -INFINITY ? 0.f : M);
-#pragma unroll
-                    for (int q = 0; q < GROUPS; ++q) {
-                        const uint32_t *r = q < 2 ? r0 + q * CHUNK : r1 + (q - 2) * CHUNK;
-                        const float add = ev[q] + ref;
-                        const uint64_t c2 = f32x2(c[q], c[q]), add2 = f32x2(add, add);
+                    sum = add_l = 0.f;
+                    for_groups([&](int q, const uint32_t (&r)[CHUNK], float c, float ev, float lf) {
+                        const float add = ev + ref;
+                        const uint64_t c2 = f32x2(c, c), add2 = f32x2(add, add);
                         uint64_t sum2 = 0;
 #pragma unroll
                         for (int k = 0; k < CHUNK; k += 2) {
@@ -580,17 +617,16 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         }
                         float sum0, sum1;
                         unpack_f32x2(sum2, sum0, sum1);
-                        sums[q] = sum0 + sum1;
-                    }
-                    again = (sums[0] + sums[1]) + (sums[2] + sums[3]) > 32768.f;   // f16 ends at 65504
+                        sum += sum0 + sum1;
+                        add_l = fmaf(sum0 + sum1, lf, add_l);
+                    });
+                    again = sum > 32768.f;       // f16 ends at 65504
                     if (!__any_sync(0xffffffffu, again))
                         break;
                 }
                 if (!ok)
                     break;
-#pragma unroll
-                for (int q = 0; q < GROUPS; ++q)
-                    l = fmaf(sums[q], lf[q], l);
+                l += add_l;
                 // A parity tells a phase from the one before only, so the wait for the last
                 // tile's product (below) needs that for the last but one's, before the last can
                 // complete.
@@ -609,8 +645,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             if (!(ok = warp_wait(C::BAR_O_DONE, (it - 1) & 1, CHUNK_ERR_SOFTMAX)))
                 break;
             tc_fence_after();
-            const int first_cta = cut ? range.owner(line.at) : cta;
-            const int last_cta = cut ? range.owner(line.at + line.span.tiles - 1) : cta;
+            const int first_cta = cut ? sh.range.owner(line.at) : cta;
+            const int last_cta = cut ? sh.range.owner(line.at + line.span.tiles - 1) : cta;
             const bool alone = first_cta == last_cta;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : M - 6.f + lg2_approx(l);
@@ -622,9 +658,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 uint32_t r[32];
                 tmem_ld32(o_addr + 32 * cc, r);
                 tmem_ld_wait(r);
+                const uint32_t marked = mark[cc * R];
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                    r[k] = (nan[cc] >> k & 1) ? 0x7fc00000u : __float_as_uint(__uint_as_float(r[k]) * inv);
+                    r[k] = (marked >> k & 1) ? 0x7fc00000u : __float_as_uint(__uint_as_float(r[k]) * inv);
                 if (alone && live) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 8)

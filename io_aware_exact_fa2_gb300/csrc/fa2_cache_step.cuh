@@ -89,26 +89,6 @@ constexpr int STEP_ERR_SOFTMAX = 12 << 8, STEP_ERR_LOAD = 13 << 8, STEP_ERR_MMA 
 
 #ifdef __CUDACC__
 
-// N consecutive 32-bit columns of this warp's 32 tensor-memory lanes; valid after ld_wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
-{
-    static_assert(N == 4, "");
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// Keeps uses of loaded registers below the wait.
-template <int N>
-__device__ __forceinline__ void tmem_pin(uint32_t (&r)[N])
-{
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        asm volatile("" : "+r"(r[i]));
-}
-
 // Largest of a warp's values (NaN only if all are).
 __device__ __forceinline__ float warp_max(float v)
 {
