@@ -20,7 +20,8 @@
 // key: the tensor pipe.  (Two e4m3 products take the time of one of f16, and K needs no
 // conversion.)  128 rows x 64 keys x D = 128 take some 540 cycles; the exponentials and the
 // rest of the softmax cost about as much issue time.  So the work has warps of its own,
-//     4 warps   softmax: one row a thread, S from and P to tensor memory
+//     8 warps   softmax: two threads a row, each half of a tile's keys; S from and P to
+//               tensor memory
 //     4 warps   values' codes to f16 operands in shared memory (swizzled)
 //     1 warp    issues the products
 //     1 warp    pages into shared memory by TMA
@@ -45,13 +46,13 @@ struct ChunkCfg {
     static constexpr int UNIT_COST = 4, MIN_TILES = 4;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = TILE;               // a tile begins at a multiple
     static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
-    static constexpr int WARP_CONVERT = 4, WARP_MMA = 8, WARP_LOAD = 9;
-    static constexpr int T = 32 * 12;                // (the last warpgroup: two idle warps)
-    // With two CTAs an SM the launch leaves 80 registers a thread, 240 for the three
+    static constexpr int WARP_CONVERT = 8, WARP_MMA = 12, WARP_LOAD = 13;
+    static constexpr int T = 32 * 16;                // (the last warpgroup: two idle warps)
+    // With two CTAs an SM the launch leaves 64 registers a thread, 256 for the four
     // warpgroups' lanes together: the softmax rises, the others give.
     static constexpr bool REG_SPLIT = CTAS == 2;
-    static constexpr int REG_SOFTMAX = 128, REG_CONVERT = 48, REG_ISSUE = 64;
-    static_assert(REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 3 * 80, "the split draws on the launch's registers");
+    static constexpr int REG_SOFTMAX = 80, REG_CONVERT = 48, REG_ISSUE = 48;
+    static_assert(2 * REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 4 * 64, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
     static constexpr int ROW = D == 64 ? 64 : 128;   // bytes of a row of codes: its swizzle span
@@ -60,13 +61,15 @@ struct ChunkCfg {
     static constexpr int Q_PANEL = R * ROW, Q_TERM = R * D;          // Q: two terms of codes
     static constexpr int V_PANEL = TILE * 128, V_BYTES = TILE * D * 2;   // V in f16: 64 columns, 128-byte rows
     static constexpr int OFF_Q = 0, OFF_V = 2 * Q_TERM, OFF_K = OFF_V + 2 * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
-    // a ring of eight tiles' group scales; of four tiles' NaN flags and NaN values by key
+    // rings: of eight tiles' group scales, of four tiles' NaN flags, of three tiles' NaN values
+    // by key (a tile is converted when the one three back has been through its softmax)
     static constexpr int NAN_WORDS = D / 32;
     static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16;
     static constexpr int OFF_FLAGS = OFF_INFO + 8 * INFO_BYTES;
     static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
-    static constexpr int OFF_MARK = OFF_NAN + 4 * NAN_BYTES;         // values of O that are NaN, by row
-    static constexpr int OFF_BAR = OFF_MARK + R * NAN_WORDS * 4;
+    static constexpr int OFF_MARK = OFF_NAN + 3 * NAN_BYTES;         // values of O that are NaN, by row
+    static constexpr int OFF_PAIR = OFF_MARK + R * NAN_WORDS * 4;    // a float of each softmax thread
+    static constexpr int OFF_BAR = OFF_PAIR + 2 * R * 4;
     static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_V_FULL = 2, BAR_V_EMPTY = 4, BAR_S_FULL = 6, BAR_P_FULL = 8,
                          BAR_O_DONE = 10, BAR_O_FREE = 11, BAR_GROUP = 12, BAR_DRAIN = 13, BAR_K_FULL = 14,
                          BAR_K_EMPTY = BAR_K_FULL + KS, BAR_RAW_FULL = BAR_K_EMPTY + KS, BAR_RAW_EMPTY = BAR_RAW_FULL + VS,
@@ -149,9 +152,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
     if (tid == 0) {
         for (int i = 0; i < C::NUM_BAR; ++i) {
-            const bool by_warps = i == C::BAR_Q_FULL || i / 2 == C::BAR_V_FULL / 2 || i / 2 == C::BAR_P_FULL / 2 ||
-                                  i == C::BAR_O_FREE || i == C::BAR_GROUP || i >= C::BAR_RAW_EMPTY;
-            mbar_init(bar(i), by_warps ? 4 : 1);
+            const bool softmax = i == C::BAR_Q_FULL || i / 2 == C::BAR_P_FULL / 2 || i == C::BAR_O_FREE || i == C::BAR_GROUP;
+            const bool convert = i / 2 == C::BAR_V_FULL / 2 || i >= C::BAR_RAW_EMPTY;
+            mbar_init(bar(i), softmax ? 8 : convert ? 4 : 1);
         }
         fence_mbar_init();
     }
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     // times a weight of 0 is NaN: such values become zeros here, and their
                     // places go to the softmax warps.  Keys that no row sees are zeros, too
                     // (without a page, what lies in their place may be anything).
-                    uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
+                    uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + g % 3 * C::NAN_BYTES);
                     bool nan = false;
 #pragma unroll
                     for (int i = 0; i < NL; ++i) {
@@ -434,36 +437,54 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             it += n;
         } while (ok && next_unit());
     } else {
-        // ============================================ softmax: one row a thread
+        // ============================================ softmax: two threads a row
         if constexpr (C::REG_SPLIT)
             setmaxnreg_inc<C::REG_SOFTMAX>();
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const int row = tid;
+        const int half = warp >> 2, row = tid & (R - 1);       // keys 32 half .. of a tile, columns D / 2 half .. of O
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float scale_log2 = a.scale * 1.4426950408889634f;
         const uint32_t o_addr = tmem + lanes + C::TM_O;
-        uint32_t group_phase = 0;
+        // the two warps of the same rows
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
+        auto pair_any = [&](bool x) -> bool {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                         "bar.red.or.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(r)
+                         : "r"(1 + (warp & 3)), "r"(static_cast<uint32_t>(x))
+                         : "memory");
+            return r != 0;
+        };
+        float *const pair = reinterpret_cast<float *>(smem + C::OFF_PAIR);   // [2][R]
+        // A wait that ran out is recorded and not waited for again: the role runs on to its end
+        // without waiting (its outputs are undefined), so that barriers between warps still match.
         bool ok = true;
+        auto wait = [&](int i, uint32_t parity) {
+            if (ok)
+                ok = warp_wait(i, parity, CHUNK_ERR_SOFTMAX);
+        };
+        uint32_t group_phase = 0;
         do {
             int tile0, tile1;
             part_of(tile0, tile1);
-            const int n = tile1 - tile0, b = line.b, h = line.h, rb = line.rb;
-            const Seq s = line.s;
+            const int n = tile1 - tile0;
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
-            const int rr = rb * R + row;
-            const bool live = rr < s.n * a.G;
-            const int tok = rr / a.G, hq = h * a.G + rr % a.G;
-            const int pos = s.kv - s.n + tok;
-            const int hi = !live ? 0 : a.causal ? pos + 1 : s.kv;
-            int lo = 0;
-            if (a.window >= 0) {
+            const int rr = line.rb * R + row;
+            const bool live = rr < line.s.n * a.G;
+            const int tok = rr / a.G, hq = line.h * a.G + rr % a.G;
+            int lo = 0, hi = 0;                                  // keys the row sees
+            {
+                const int pos = line.s.kv - line.s.n + tok;
+                if (live)
+                    hi = a.causal ? pos + 1 : line.s.kv;
                 const long long x = static_cast<long long>(pos) - a.window;
-                lo = x > 0 ? static_cast<int>(x) : 0;
+                lo = a.window >= 0 && x > 0 ? static_cast<int>(x) : 0;
             }
             // ---- this row of Q as two e4m3 terms, times the power of two that brings its
-            // largest magnitude to [224, 448)
+            // largest magnitude to [224, 448); each thread stores half of it
             int e;
             {
-                const uint16_t *q = static_cast<const uint16_t *>(a.q) + b * a.q_sb + hq * a.q_sh + tok * a.q_sl;
+                const uint16_t *q = static_cast<const uint16_t *>(a.q) + line.b * a.q_sb + hq * a.q_sh + tok * a.q_sl;
                 uint32_t top = 0;
 #pragma unroll 8
                 for (int c = 0; c < D / 8; ++c) {
@@ -478,21 +499,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 e = e < -126 ? -126 : e;
                 // a row with an infinity or NaN has no finite scores: make it NaN
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
-                if (unit > 0 && !(ok = warp_wait(C::BAR_Q_EMPTY, (unit - 1) & 1, CHUNK_ERR_SOFTMAX)))
-                    break;
+                if (unit > 0)
+                    wait(C::BAR_Q_EMPTY, (unit - 1) & 1);
 #pragma unroll 2
-                for (int c = 0; c < D / 16; ++c) {
+                for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
                     uint32_t t0[4], t1[4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c * 2 + half) : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c * 2 + i) : make_uint4(0, 0, 0, 0);
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int k = 0; k < 4; k += 2) {
                             uint32_t y0 = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
                             uint32_t y1 = pack_f16x2(__uint_as_float(w[k + 1] << 16) * f, __uint_as_float(w[k + 1] & 0xffff0000u) * f);
-                            t0[half * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
-                            t1[half * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                            t0[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                            t1[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
                         }
                     }
                     const int panel = c * 16 / C::ROW, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
@@ -505,26 +526,25 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             }
 
             const float scale_row = scale_log2 * pow2i(e);
-            float M = -INFINITY, l = 0.f;
-            // values of O that a visible NaN value makes NaN (this thread's alone)
+            float M = -INFINITY, l = 0.f;                        // (M: the same in both threads)
+            // values of O that a visible NaN value makes NaN (the first thread's to set)
             uint32_t *const mark = reinterpret_cast<uint32_t *>(smem + C::OFF_MARK) + row;   // word q: [q * R]
+            if (half == 0)
 #pragma unroll
-            for (int q = 0; q < C::NAN_WORDS; ++q)
-                mark[q * R] = 0;
+                for (int q = 0; q < C::NAN_WORDS; ++q)
+                    mark[q * R] = 0;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = it + j, buf = g & 1;
-                if (!(ok = warp_wait(C::BAR_S_FULL + buf, g >> 1 & 1, CHUNK_ERR_SOFTMAX)))
-                    break;
+                wait(C::BAR_S_FULL + buf, g >> 1 & 1);
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lanes + C::TM_S + buf * TILE;
                 const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES);
                 const int pos0 = from + j * TILE;
                 const bool whole = is_whole(smem, g);
                 if (!whole) {            // NaN values, once the tile's are converted
-                    if (!(ok = warp_wait(C::BAR_V_FULL + buf, g >> 1 & 1, CHUNK_ERR_SOFTMAX)))
-                        break;
-                    if (*reinterpret_cast<const uint32_t *>(smem + C::OFF_FLAGS + (g & 3) * 4)) {
-                        const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
+                    wait(C::BAR_V_FULL + buf, g >> 1 & 1);
+                    if (half == 0 && *reinterpret_cast<const uint32_t *>(smem + C::OFF_FLAGS + (g & 3) * 4)) {
+                        const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + g % 3 * C::NAN_BYTES);
 #pragma unroll 1
                         for (int k = 0; k < TILE; ++k)
                             if (pos0 + k >= lo && pos0 + k < hi)
@@ -533,41 +553,40 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                                     mark[q * R] |= map[k * C::NAN_WORDS + q];
                     }
                 }
+                // this thread's scores, 16 at a time; those that the row does not see are -inf
+                auto for_groups = [&](auto f) {
+                    uint32_t r[2][CHUNK];
+                    tmem_ld(s_addr + half * (TILE / 2), r[0]);
+                    tmem_ld(s_addr + half * (TILE / 2) + CHUNK, r[1]);
+                    tmem_wait_ld();
+                    tmem_pin(r[0]);
+                    tmem_pin(r[1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 scales = info[half * 2 + i];
+                        if (!whole) {
+                            const uint32_t word = __float_as_uint(scales.w);
+                            const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
+                            const int key0 = pos0 + half * (TILE / 2) + i * CHUNK;
+#pragma unroll
+                            for (int k = 0; k < CHUNK; ++k) {
+                                const bool see = page && key0 + k >= lo && key0 + k < hi;
+                                r[i][k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[i][k];
+                            }
+                        }
+                        // (not 0: a hidden score is -inf * c)
+                        f(i, r[i], fmaxf(scale_row * scales.x, 1.17549435e-38f), scales.y, scales.z);
+                    }
+                };
                 // Weights as f16 pairs, by the maximum so far.  Their sum tells whether one is
                 // too large for it: only then (and for a row's first keys) is the tile's maximum
                 // taken, O and l brought to it, and the weights taken again.
-                uint32_t p[32];
+                uint32_t p[16];
                 float sum, add_l;
                 bool waited = j == 0;
-                bool again = M == -INFINITY && lo < pos0 + TILE && hi > pos0;
-                // A group of 16 scores at a time, the next one on its way from tensor memory; those
-                // that the row does not see are -inf.
-                auto for_groups = [&](auto f) {
-                    uint32_t r[2][CHUNK];
-                    tmem_ld(s_addr, r[0]);
-#pragma unroll
-                    for (int q = 0; q < GROUPS; ++q) {
-                        tmem_wait_ld();
-                        tmem_pin(r[q & 1]);
-                        if (q + 1 < GROUPS)
-                            tmem_ld(s_addr + (q + 1) * CHUNK, r[(q + 1) & 1]);
-                        if (!whole) {
-                            const uint32_t word = __float_as_uint(info[q].w);
-                            const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
-#pragma unroll
-                            for (int k = 0; k < CHUNK; ++k) {
-                                const int key = pos0 + q * CHUNK + k;
-                                const bool see = page && key >= lo && key < hi;
-                                r[q & 1][k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[q & 1][k];
-                            }
-                        }
-                        const float4 scales = info[q];
-                        // (not 0: a hidden score is -inf * c)
-                        f(q, r[q & 1], fmaxf(scale_row * scales.x, 1.17549435e-38f), scales.y, scales.z);
-                    }
-                };
-                for (;;) {
-                    if (__any_sync(0xffffffffu, again)) {
+                bool again = __any_sync(0xffffffffu, M == -INFINITY && lo < pos0 + TILE && hi > pos0);
+                for (int attempt = 0; attempt < 2; ++attempt) {
+                    if (again) {
                         float top = -INFINITY;   // of x + ev
                         for_groups([&](int, const uint32_t (&r)[CHUNK], float c, float ev, float) {
                             float t = __uint_as_float(r[0]);
@@ -577,6 +596,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             t = fmaxf(t, __uint_as_float(r[CHUNK - 1]));
                             top = fmaxf(top, fmaf(t, c, ev));
                         });
+                        pair[tid] = top;
+                        pair_sync();
+                        top = fmaxf(top, pair[tid ^ R]);
                         float f = 1.f;
                         if (top > M) {
                             f = ex2_approx(M - top);
@@ -584,25 +606,26 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             l *= f;
                         }
                         if (j > 0) {             // O in tensor memory stands for the old maximum
-                            if (!waited && !(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
-                                break;
+                            if (!waited)
+                                wait(C::BAR_O_DONE, (g - 1) & 1);
                             waited = true;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int cc = 0; cc < D / 32; ++cc) {
-                                uint32_t o[32];
-                                tmem_ld32(o_addr + 32 * cc, o);
-                                tmem_ld_wait(o);
+                            for (int cc = half * (D / 32); cc < (half + 1) * (D / 32); ++cc) {
+                                uint32_t o[16];
+                                tmem_ld(o_addr + 16 * cc, o);
+                                tmem_wait_ld();
+                                tmem_pin(o);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
+                                for (int k = 0; k < 16; ++k)
                                     o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                tmem_st32(o_addr + 32 * cc, o);
+                                tmem_st16(o_addr + 16 * cc, o);
                             }
                         }
                     }
                     const float ref = 6.f - (M == -INFINITY ? 0.f : M);
                     sum = add_l = 0.f;
-                    for_groups([&](int q, const uint32_t (&r)[CHUNK], float c, float ev, float lf) {
+                    for_groups([&](int i, const uint32_t (&r)[CHUNK], float c, float ev, float lf) {
                         const float add = ev + ref;
                         const uint64_t c2 = f32x2(c, c), add2 = f32x2(add, add);
                         uint64_t sum2 = 0;
@@ -613,111 +636,112 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             x0 = ex2_approx(x0);
                             x1 = ex2_approx(x1);
                             sum2 = add_f32x2(sum2, f32x2(x0, x1));
-                            p[q * 8 + k / 2] = pack_f16x2(x0, x1);
+                            p[i * 8 + k / 2] = pack_f16x2(x0, x1);
                         }
                         float sum0, sum1;
                         unpack_f32x2(sum2, sum0, sum1);
                         sum += sum0 + sum1;
                         add_l = fmaf(sum0 + sum1, lf, add_l);
                     });
-                    again = sum > 32768.f;       // f16 ends at 65504
-                    if (!__any_sync(0xffffffffu, again))
+                    // (f16 ends at 65504; by the tile's own maximum the sum is 2^11 at most.)  The
+                    // weights go over the scores, so both threads have read theirs after this.
+                    again = pair_any(sum > 32768.f);
+                    if (!again)
                         break;
                 }
-                if (!ok)
-                    break;
                 l += add_l;
                 // A parity tells a phase from the one before only, so the wait for the last
                 // tile's product (below) needs that for the last but one's, before the last can
                 // complete.
-                if (!waited && j == n - 1 && !(ok = warp_wait(C::BAR_O_DONE, (g - 1) & 1, CHUNK_ERR_SOFTMAX)))
-                    break;
-                tmem_st32(s_addr, p);
+                if (!waited && j == n - 1)
+                    wait(C::BAR_O_DONE, (g - 1) & 1);
+                tmem_st16(s_addr + half * 16, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(C::BAR_P_FULL + buf);
             }
-            if (!ok)
-                break;
 
             // ---- O out of tensor memory: the unit's rows, or this part of them
             it += n;
-            if (!(ok = warp_wait(C::BAR_O_DONE, (it - 1) & 1, CHUNK_ERR_SOFTMAX)))
-                break;
+            pair[tid] = l;
+            pair_sync();
+            l = (half ? pair[row] : l) + (half ? l : pair[R + row]);   // (in one order)
+            wait(C::BAR_O_DONE, (it - 1) & 1);
             tc_fence_after();
             const int first_cta = cut ? sh.range.owner(line.at) : cta;
             const int last_cta = cut ? sh.range.owner(line.at + line.span.tiles - 1) : cta;
             const bool alone = first_cta == last_cta;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : M - 6.f + lg2_approx(l);
-            uint16_t *const o = static_cast<uint16_t *>(a.o) + b * a.o_sb + hq * a.o_sh + tok * a.o_sl;
+            uint16_t *const o = static_cast<uint16_t *>(a.o) + line.b * a.o_sb + hq * a.o_sh + tok * a.o_sl;
             float *const part =
                 cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
+#pragma unroll 1
+            for (int cc = half * (D / 32); cc < (half + 1) * (D / 32); ++cc) {   // 16 columns
+                uint32_t r[16];
+                tmem_ld(o_addr + 16 * cc, r);
+                tmem_wait_ld();
+                tmem_pin(r);
+                const uint32_t marked = mark[(cc >> 1) * R] >> (cc & 1) * 16;
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t r[32];
-                tmem_ld32(o_addr + 32 * cc, r);
-                tmem_ld_wait(r);
-                const uint32_t marked = mark[cc * R];
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
+                for (int k = 0; k < 16; ++k)
                     r[k] = (marked >> k & 1) ? 0x7fc00000u : __float_as_uint(__uint_as_float(r[k]) * inv);
                 if (alone && live) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4 *>(o + cc * 32 + k) =
+                    for (int k = 0; k < 16; k += 8)
+                        *reinterpret_cast<uint4 *>(o + cc * 16 + k) =
                             make_uint4(pack_bf16x2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
                                        pack_bf16x2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])),
                                        pack_bf16x2(__uint_as_float(r[k + 4]), __uint_as_float(r[k + 5])),
                                        pack_bf16x2(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7])));
                 } else if (!alone) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4 *>(part + row * D + cc * 32 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                    for (int k = 0; k < 16; k += 4)
+                        *reinterpret_cast<uint4 *>(part + row * D + cc * 16 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
                 }
             }
             tc_fence_before();
             warp_arrive(C::BAR_O_FREE);
             auto write_lse = [&](int r, float v) {
-                const int x = rb * R + r;
-                if (x < s.n * a.G)
-                    a.lse[(static_cast<long long>(b) * a.Hq + h * a.G + x % a.G) * a.Lq + x / a.G] = v * 0.69314718055994531f;
+                const int x = line.rb * R + r;
+                if (x < line.s.n * a.G)
+                    a.lse[(static_cast<long long>(line.b) * a.Hq + line.h * a.G + x % a.G) * a.Lq + x / a.G] =
+                        v * 0.69314718055994531f;
             };
             if (alone) {
-                write_lse(row, lse2);
+                if (half == 0)
+                    write_lse(row, lse2);
             } else {
-                part[R * D + row] = lse2;
+                if (half == 0)
+                    part[R * D + row] = lse2;
                 // the CTA whose part is the last to arrive merges them
-                auto group = [&]() -> bool {
+                auto group = [&] {
                     warp_arrive(C::BAR_GROUP);
-                    return warp_wait(C::BAR_GROUP, group_phase++ & 1, CHUNK_ERR_SOFTMAX);
+                    wait(C::BAR_GROUP, group_phase++ & 1);
                 };
                 __threadfence();
-                if (!(ok = group()))
-                    break;
+                group();
                 volatile int *const last = reinterpret_cast<int *>(smem + C::OFF_MISC + 4);
                 if (tid == 0) {
                     *last = atomicAdd(parts.counters + first_cta, 1) == last_cta - first_cta;
                     if (*last)
                         parts.counters[first_cta] = 0;
                 }
-                if (!(ok = group()))
-                    break;
+                group();
                 if (*last) {
                     __threadfence();
                     auto write_o = [&](int r, int u, const float4 &v) {
-                        const int x = rb * R + r;
-                        if (x >= s.n * a.G)
-                            return;
-                        uint16_t *to = static_cast<uint16_t *>(a.o) + b * a.o_sb + (h * a.G + x % a.G) * a.o_sh +
+                        const int x = line.rb * R + r;
+                        uint16_t *to = static_cast<uint16_t *>(a.o) + line.b * a.o_sb + (line.h * a.G + x % a.G) * a.o_sh +
                                        static_cast<long long>(x / a.G) * a.o_sl;
                         *reinterpret_cast<uint2 *>(to + u * 4) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     };
-                    const int live_rows = s.n * a.G - rb * R;
-                    merge_parts<C>(parts, first_cta, last_cta, live_rows < R ? live_rows : R, tid, 128, write_o, write_lse);
+                    const int live_rows = line.s.n * a.G - line.rb * R;
+                    merge_parts<C>(parts, first_cta, last_cta, live_rows < R ? live_rows : R, tid, 2 * R, write_o, write_lse);
                 }
             }
             ++unit;
+            pair_sync();          // (the marks are read)
         } while (next_unit());
         tmem_st_wait();   // a loop left early may leave stores in flight
     }
