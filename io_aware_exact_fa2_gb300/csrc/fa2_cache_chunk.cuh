@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 
     const uint64_t limit = a.wait_limit_ns;
     auto warp_wait = [&](int i, uint32_t parity, int code) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, a.err, code | i, limit));
+        return wait_phase(bar(i), parity, a.err, code | i, limit);
     };
     auto warp_arrive = [&](int i) {
         __syncwarp();

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     bool ok = true;
     auto warp_wait = [&](int i, uint32_t parity, int code) {
         if (ok)
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, a.err, code | i, a.wait_limit_ns));
+            ok = wait_phase(bar(i), parity, a.err, code | i, a.wait_limit_ns);
     };
     auto warp_arrive = [&](int i) {
         __syncwarp();

@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "fa2_cache.cuh"
+#include "sm103_ptx.cuh"
 
 namespace fa2 {
 namespace cache {
@@ -31,6 +32,33 @@ inline bool page_map(EncodeTiled encode, CUtensorMap *m, const Half &x, const Vi
 }
 
 #ifdef __CUDACC__
+// Waits for the phase of parity `parity` of an mbarrier to complete, as a whole warp; false
+// (and `code` in *err, first writer wins) when `limit_ns` passes first.  The hint lets the
+// hardware suspend the warp for up to 20 us at a time: without one the waits of a kernel whose
+// warps each do one part of the work took a third of its issue slots.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int *err, int code, uint64_t limit_ns)
+{
+    auto done = [&]() -> bool {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity), "n"(20000)
+                     : "memory");
+        return __all_sync(0xffffffffu, ok);
+    };
+    if (done())
+        return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!done())
+        if (__any_sync(0xffffffffu, ptx::globaltimer_ns() - t0 > limit_ns)) {
+            atomicCAS(err, 0, code);
+            return false;
+        }
+    return true;
+}
+
 // N consecutive 32-bit columns of this warp's 32 tensor-memory lanes; valid after the wait.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4])
 {
