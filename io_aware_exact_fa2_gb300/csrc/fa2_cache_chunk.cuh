@@ -42,8 +42,8 @@ template <int D_>
 struct ChunkCfg {
     static constexpr int D = D_;
     static constexpr int R = 128;                    // query rows of a unit
-    static constexpr int TILE = 64;                  // keys
-    static constexpr int UNIT_COST = 4, MIN_TILES = 4;   // see fa2_cache_line.cuh
+    static constexpr int TILE = 128;                 // keys
+    static constexpr int UNIT_COST = 2, MIN_TILES = 2;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = TILE;               // a tile begins at a multiple
     static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
     static constexpr int WARP_CONVERT = 8, WARP_MMA = 12, WARP_LOAD = 13;
@@ -51,23 +51,25 @@ struct ChunkCfg {
     // With two CTAs an SM the launch leaves 64 registers a thread, 256 for the four
     // warpgroups' lanes together: the softmax rises, the others give.
     static constexpr bool REG_SPLIT = CTAS == 2;
-    static constexpr int REG_SOFTMAX = 80, REG_CONVERT = 48, REG_ISSUE = 48;
+    static constexpr int REG_SOFTMAX = 88, REG_CONVERT = 40, REG_ISSUE = 40;
     static_assert(2 * REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 4 * 64, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
     static constexpr int ROW = D == 64 ? 64 : 128;   // bytes of a row of codes: its swizzle span
     static constexpr int PANELS = D / ROW, PANEL = TILE * ROW;       // of a stage of codes
-    static constexpr int STAGE = TILE * D, KS = 2, VS = 3;           // stages of keys, of values
+    static constexpr int STAGE = TILE * D, KS = D == 64 ? 2 : 1, VS = D == 64 ? 2 : 1;   // stages of keys, of values
+    static constexpr int SB = D == 256 ? 2 : 1;                      // buffers of S
     static constexpr int Q_PANEL = R * ROW, Q_TERM = R * D;          // Q: two terms of codes
-    static constexpr int V_PANEL = TILE * 128, V_BYTES = TILE * D * 2;   // V in f16: 64 columns, 128-byte rows
+    // V in f16, each half of a tile's keys a buffer: panels of 64 columns, 128-byte rows
+    static constexpr int HALF = TILE / 2, V_PANEL = HALF * 128, V_BYTES = HALF * D * 2;
     static constexpr int OFF_Q = 0, OFF_V = 2 * Q_TERM, OFF_K = OFF_V + 2 * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
-    // rings: of eight tiles' group scales, of four tiles' NaN flags, of three tiles' NaN values
-    // by key (a tile is converted when the one three back has been through its softmax)
+    // Rings of tiles: group scales, NaN flags, NaN values by key.  (A tile is loaded, and the
+    // one after it converted, when the one two back has been through its softmax.)
     static constexpr int NAN_WORDS = D / 32;
     static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16;
-    static constexpr int OFF_FLAGS = OFF_INFO + 8 * INFO_BYTES;
+    static constexpr int OFF_FLAGS = OFF_INFO + 4 * INFO_BYTES;
     static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
-    static constexpr int OFF_MARK = OFF_NAN + 3 * NAN_BYTES;         // values of O that are NaN, by row
+    static constexpr int OFF_MARK = OFF_NAN + 2 * NAN_BYTES;         // values of O that are NaN, by row
     static constexpr int OFF_PAIR = OFF_MARK + R * NAN_WORDS * 4;    // a float of each softmax thread
     static constexpr int OFF_BAR = OFF_PAIR + 2 * R * 4;
     static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_V_FULL = 2, BAR_V_EMPTY = 4, BAR_S_FULL = 6, BAR_P_FULL = 8,
@@ -77,7 +79,7 @@ struct ChunkCfg {
     static constexpr int OFF_MISC = OFF_BAR + NUM_BAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // 1024: operand alignment
 
-    static constexpr int TM_S = 0, TM_O = 2 * TILE;
+    static constexpr int TM_S = 0, TM_O = SB * TILE;
     static constexpr int TMEM_COLS = D <= 128 ? 256 : 512;
 
     // kind::f16 with f16 A and B (formats 0), fp32 accumulator
@@ -85,7 +87,7 @@ struct ChunkCfg {
     {
         return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(R >> 4) << 24);
     }
-    static_assert(CTAS * (SMEM_BYTES + 1024 + 512) <= 228 * 1024 && CTAS * TMEM_COLS <= 512 && 2 * TILE + D <= TMEM_COLS, "an SM holds CTAS of them");
+    static_assert(CTAS * (SMEM_BYTES + 1024 + 512) <= 228 * 1024 && CTAS * TMEM_COLS <= 512 && SB * TILE + D <= TMEM_COLS, "an SM holds CTAS of them");
 };
 
 // Error codes of waits that ran out (bits 8-11 the waiting role).
@@ -190,10 +192,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     };
     // what the loading warp says of tile g: a group's scales, and whether every row sees every key
     auto group_word = [](const uint8_t *smem, uint32_t g, int q) {
-        return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES)[q * 4 + 3];
+        return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES)[q * 4 + 3];
     };
     auto is_whole = [](const uint8_t *smem, uint32_t g) {
-        return *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES + GROUPS * 16) != 0;
+        return *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES + GROUPS * 16) != 0;
     };
     uint32_t it = 0;       // tiles before the present unit's first: buffers alternate by tile
     uint32_t unit = 0;
@@ -220,12 +222,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk) {
                             const int panel = kk * 32 / C::ROW, col = kk * 32 % C::ROW;
-                            mma_ss<true>(tmem + C::TM_S + (g & 1) * TILE,
+                            mma_ss<true>(tmem + C::TM_S + g % C::SB * TILE,
                                          desc_q + ((term * C::Q_TERM + panel * C::Q_PANEL + col) >> 4),
                                          dk + ((panel * C::PANEL + col) >> 4), idesc_e4m3_f32(R, TILE, false, false),
                                          term > 0 || kk > 0);
                         }
-                    mma_commit(bar(C::BAR_S_FULL + (g & 1)));
+                    mma_commit(bar(C::BAR_S_FULL + g % C::SB));
                     mma_commit(bar(C::BAR_K_EMPTY + stage));
                     if (last)
                         mma_commit(bar(C::BAR_Q_EMPTY));
@@ -234,23 +236,27 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 return true;
             };
             auto issue_pv = [&](uint32_t g, bool start) -> bool {   // O += P V of tile g
-                const uint32_t buf = g & 1;
                 // a unit's first product overwrites O: the one before has been read out
-                if (!warp_wait(C::BAR_V_FULL + buf, g >> 1 & 1, CHUNK_ERR_MMA) ||
-                    !warp_wait(C::BAR_P_FULL + buf, g >> 1 & 1, CHUNK_ERR_MMA) ||
+                if (!warp_wait(C::BAR_P_FULL + g % C::SB, g / C::SB & 1, CHUNK_ERR_MMA) ||
                     (start && unit > 0 && !warp_wait(C::BAR_O_FREE, (unit - 1) & 1, CHUNK_ERR_MMA)))
                     return false;
-                tc_fence_after();
-                if (leader) {
-                    const uint64_t dv = desc_v + (buf * C::V_BYTES >> 4);
+                for (int half = 0; half < 2; ++half) {
+                    if (!warp_wait(C::BAR_V_FULL + half, g & 1, CHUNK_ERR_MMA))
+                        return false;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t dv = desc_v + (half * C::V_BYTES >> 4);
+                        const uint32_t p = tmem + C::TM_S + g % C::SB * TILE + half * (C::HALF / 2);
 #pragma unroll
-                    for (int kk = 0; kk < TILE / 16; ++kk)
-                        mma_ts(tmem + C::TM_O, tmem + C::TM_S + buf * TILE + kk * 8, dv + (kk * 16 * 128 >> 4),
-                               C::idesc(D, true), !start || kk > 0);
-                    mma_commit(bar(C::BAR_O_DONE));
-                    mma_commit(bar(C::BAR_V_EMPTY + buf));
+                        for (int kk = 0; kk < C::HALF / 16; ++kk)
+                            mma_ts(tmem + C::TM_O, p + kk * 8, dv + (kk * 16 * 128 >> 4), C::idesc(D, true),
+                                   !start || half > 0 || kk > 0);
+                        mma_commit(bar(C::BAR_V_EMPTY + half));
+                        if (half)
+                            mma_commit(bar(C::BAR_O_DONE));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 return true;
             };
             bool ok = true;
@@ -259,12 +265,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 part_of(tile0, tile1);
                 const int n = tile1 - tile0;
                 ok = warp_wait(C::BAR_Q_FULL, unit & 1, CHUNK_ERR_MMA);
-                for (int j = 0; j < 2 && j < n && ok; ++j)
+                for (int j = 0; j < C::SB && j < n && ok; ++j)
                     ok = issue_s(it + j, j == n - 1);
                 for (int j = 0; j < n && ok; ++j) {
                     ok = issue_pv(it + j, j == 0);
-                    if (ok && j + 2 < n)
-                        ok = issue_s(it + j + 2, j + 2 == n - 1);
+                    if (ok && j + C::SB < n)
+                        ok = issue_s(it + j + C::SB, j + C::SB == n - 1);
                 }
                 it += n;
                 ++unit;
@@ -276,8 +282,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             warp_wait(C::BAR_DRAIN, 0, CHUNK_ERR_DRAIN);
         } else if (warp == C::WARP_LOAD) {
             // ======================================== pages -> stages
-            const int box_shift = a.c.page_shift < 6 ? a.c.page_shift : 6;   // rows of a box
-            const int boxes_shift = 6 - box_shift;             // boxes of a tile
+            const int box_shift = a.c.page_shift;              // rows of a box: a page
+            const int boxes_shift = 7 - box_shift;             // boxes of a tile
             const uint32_t box_bytes = static_cast<uint32_t>(D) << box_shift;
             const int in_tile = lane & ((1 << boxes_shift) - 1);
             const uint32_t offset = static_cast<uint32_t>(in_tile) * C::ROW << box_shift;   // in each panel
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
                 int all_lo, all_hi;
                 line.seen_by_all(a, all_lo, all_hi);
-                // A lane has one of 32 boxes, those of the next 8 to 32 tiles: the table's
+                // A lane has one of 32 boxes, those of the next 4 to 32 tiles: the table's
                 // entries come two such batches ahead, their scales one.
                 auto pos_at = [&](int tile) { return from + tile * TILE + (lane << box_shift); };
                 auto pages = [&](int tile) {                   // -1: none, or not seen
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const long long i = static_cast<long long>(page) * a.c.H + h;
                     return a.c.k.scale[i] | static_cast<uint32_t>(a.c.v.scale[i]) << 8 | PAGE_BIT;
                 };
-                int id = pages(0), id_next = pages(batch_tiles), id_after = pages(2 * batch_tiles), slot = 0;
+                int id = pages(0), id_next = pages(batch_tiles), id_after = pages(2 * batch_tiles);
                 uint32_t sc = scales(id), sc_next = scales(id_next);
                 float4 info = make_float4(0.f, 0.f, 0.f, 0.f);
                 bool fine = false;
@@ -321,7 +327,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             sc_next = scales(id_next);
                             id_after = pages(j + 2 * batch_tiles);
                         }
-                        slot = pos_at(j) & ((1 << a.c.page_shift) - 1);
                         // for the box's groups of 16 keys: 2^ek, ev, 2^-ev, and the scales' word
                         // (which tells a NaN scale)
                         const int kb = sc & 255, vb = sc >> 8 & 255;
@@ -337,8 +342,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * box_bytes;
                     const int pos0 = from + j * TILE;
                     const bool whole = __all_sync(0xffffffffu, !mine || fine) && pos0 >= all_lo && pos0 + TILE <= all_hi;
-                    // (the tile eight back is done with: its values' stage came back twice)
-                    uint8_t *const to = smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES;
+                    uint8_t *const to = smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES;
                     if (mine)
                         for (int k = 0; k < 1 << (box_shift - 4); ++k)
                             reinterpret_cast<float4 *>(to)[(in_tile << (box_shift - 4)) + k] = info;
@@ -353,9 +357,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     if (mine && id >= 0)
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p) {
-                            tma_load_4d(base + C::OFF_K + ks * C::STAGE + p * C::PANEL + offset, &k_map, p * 128, slot, h, id,
+                            tma_load_4d(base + C::OFF_K + ks * C::STAGE + p * C::PANEL + offset, &k_map, p * 128, 0, h, id,
                                         bar(C::BAR_K_FULL + ks));
-                            tma_load_4d(base + C::OFF_RAW + vs * C::STAGE + p * C::PANEL + offset, &v_map, p * 128, slot, h, id,
+                            tma_load_4d(base + C::OFF_RAW + vs * C::STAGE + p * C::PANEL + offset, &v_map, p * 128, 0, h, id,
                                         bar(C::BAR_RAW_FULL + vs));
                         }
                     __syncwarp();
@@ -376,12 +380,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             setmaxnreg_dec<C::REG_CONVERT>();
         // Eight lanes take eight rows of one 16-byte column: the swizzles of both sides spread
         // them over all banks.
-        constexpr int NL = D / 32;                       // 16-byte pieces a thread takes
+        constexpr int NL = D / 32;                       // 16-byte pieces a thread takes of half a tile
         const int w = warp - C::WARP_CONVERT;
         const int row0 = w * 8 + (lane & 7);             // piece i: row row0 + 32 (i & 1), column 4 (i / 2) + c
         const int c = lane >> 3;
-        auto raw_at = [&](uint32_t stage, int i) {
-            const int row = row0 + 32 * (i & 1), col = (i >> 1) * 4 + c;
+        auto raw_at = [&](uint32_t stage, int half, int i) {
+            const int row = half * C::HALF + row0 + 32 * (i & 1), col = (i >> 1) * 4 + c;
             const int panel = col * 16 / C::ROW, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
             return base + C::OFF_RAW + stage * C::STAGE + panel * C::PANEL + row * C::ROW + ((col % (C::ROW / 16) ^ x) << 4);
         };
@@ -392,47 +396,53 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             const int n = tile1 - tile0;
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
             const int stop = line.span.hi < from + n * TILE ? line.span.hi : from + n * TILE;
-            for (int j = 0; j < n; ++j) {
-                const uint32_t g = it + j, buf = g & 1, stage = g % C::VS;
-                const int pos0 = from + j * TILE;
+            for (int j = 0; j < n && ok; ++j) {
+                const uint32_t g = it + j, stage = g % C::VS;
                 if (!(ok = warp_wait(C::BAR_RAW_FULL + stage, g / C::VS & 1, CHUNK_ERR_CONVERT)))
                     break;
-                uint4 v[NL];
+                const bool whole = is_whole(smem, g);
+                bool nan = false;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint4 v[NL];
 #pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    ld_shared_v4(raw_at(stage, i), v[i].x, v[i].y, v[i].z, v[i].w);
-                if (!is_whole(smem, g)) {
-                    // Rows of the block see different keys of this tile, and a NaN value
-                    // times a weight of 0 is NaN: such values become zeros here, and their
-                    // places go to the softmax warps.  Keys that no row sees are zeros, too
-                    // (without a page, what lies in their place may be anything).
-                    uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + g % 3 * C::NAN_BYTES);
-                    bool nan = false;
+                    for (int i = 0; i < NL; ++i)
+                        ld_shared_v4(raw_at(stage, half, i), v[i].x, v[i].y, v[i].z, v[i].w);
+                    if (!whole) {
+                        // Rows of the block see different keys of this tile, and a NaN value
+                        // times a weight of 0 is NaN: such values become zeros here, and their
+                        // places go to the softmax warps.  Keys that no row sees are zeros, too
+                        // (without a page, what lies in their place may be anything).
+                        uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + (g & 1) * C::NAN_BYTES);
 #pragma unroll
-                    for (int i = 0; i < NL; ++i) {
-                        const int row = row0 + 32 * (i & 1), pos = pos0 + row;
-                        const uint32_t sc = group_word(smem, g, row >> 4);
-                        const bool seen = (sc & PAGE_BIT) && pos >= line.span.lo && pos < stop;
-                        uint32_t m = nan_bits(v[i].x) | nan_bits(v[i].y) << 4 | nan_bits(v[i].z) << 8 | nan_bits(v[i].w) << 12;
-                        m = !seen ? 0 : (sc >> 8 & 255) == 255 ? 0xffffu : m;
-                        v[i] = seen ? make_uint4(without_nan(v[i].x), without_nan(v[i].y), without_nan(v[i].z), without_nan(v[i].w))
-                                    : make_uint4(0, 0, 0, 0);
-                        nan |= m != 0;
-                        map[row * (D / 16) + (i >> 1) * 4 + c] = static_cast<uint16_t>(m);
+                        for (int i = 0; i < NL; ++i) {
+                            const int row = half * C::HALF + row0 + 32 * (i & 1), pos = from + j * TILE + row;
+                            const uint32_t sc = group_word(smem, g, row >> 4);
+                            const bool seen = (sc & PAGE_BIT) && pos >= line.span.lo && pos < stop;
+                            uint32_t m = nan_bits(v[i].x) | nan_bits(v[i].y) << 4 | nan_bits(v[i].z) << 8 | nan_bits(v[i].w) << 12;
+                            m = !seen ? 0 : (sc >> 8 & 255) == 255 ? 0xffffu : m;
+                            v[i] = seen ? make_uint4(without_nan(v[i].x), without_nan(v[i].y), without_nan(v[i].z), without_nan(v[i].w))
+                                        : make_uint4(0, 0, 0, 0);
+                            nan |= m != 0;
+                            map[row * (D / 16) + (i >> 1) * 4 + c] = static_cast<uint16_t>(m);
+                        }
+                        if (half) {
+                            nan = __any_sync(0xffffffffu, nan);
+                            if (lane == 0)   // one byte a warp
+                                smem[C::OFF_FLAGS + (g & 3) * 4 + w] = nan;
+                        }
                     }
-                    nan = __any_sync(0xffffffffu, nan);
-                    if (lane == 0)   // one byte a warp
-                        smem[C::OFF_FLAGS + (g & 3) * 4 + w] = nan;
-                }
-                warp_arrive(C::BAR_RAW_EMPTY + stage);
-                if (g >= 2 && !(ok = warp_wait(C::BAR_V_EMPTY + buf, (g >> 1 & 1) ^ 1, CHUNK_ERR_CONVERT)))
-                    break;
+                    if (half)
+                        warp_arrive(C::BAR_RAW_EMPTY + stage);
+                    if (g >= 1 && !(ok = warp_wait(C::BAR_V_EMPTY + half, (g - 1) & 1, CHUNK_ERR_CONVERT)))
+                        break;
 #pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    store_f16(base + C::OFF_V + buf * C::V_BYTES + (i >> 1) * C::V_PANEL + (row0 + 32 * (i & 1)) * 128, row0, c * 2,
-                              v[i]);
-                fence_proxy_async_shared();
-                warp_arrive(C::BAR_V_FULL + buf);
+                    for (int i = 0; i < NL; ++i)
+                        store_f16(base + C::OFF_V + half * C::V_BYTES + (i >> 1) * C::V_PANEL + (row0 + 32 * (i & 1)) * 128, row0,
+                                  c * 2, v[i]);
+                    fence_proxy_async_shared();
+                    warp_arrive(C::BAR_V_FULL + half);
+                }
             }
             it += n;
         } while (ok && next_unit());
@@ -440,7 +450,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         // ============================================ softmax: two threads a row
         if constexpr (C::REG_SPLIT)
             setmaxnreg_inc<C::REG_SOFTMAX>();
-        const int half = warp >> 2, row = tid & (R - 1);       // keys 32 half .. of a tile, columns D / 2 half .. of O
+        const int half = warp >> 2, row = tid & (R - 1);       // keys 64 half .. of a tile, columns D / 2 half .. of O
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float scale_log2 = a.scale * 1.4426950408889634f;
         const uint32_t o_addr = tmem + lanes + C::TM_O;
@@ -534,17 +544,18 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 for (int q = 0; q < C::NAN_WORDS; ++q)
                     mark[q * R] = 0;
             for (int j = 0; j < n; ++j) {
-                const uint32_t g = it + j, buf = g & 1;
-                wait(C::BAR_S_FULL + buf, g >> 1 & 1);
+                const uint32_t g = it + j, buf = g % C::SB;
+                wait(C::BAR_S_FULL + buf, g / C::SB & 1);
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lanes + C::TM_S + buf * TILE;
-                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 7) * C::INFO_BYTES);
+                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES);
                 const int pos0 = from + j * TILE;
                 const bool whole = is_whole(smem, g);
                 if (!whole) {            // NaN values, once the tile's are converted
-                    wait(C::BAR_V_FULL + buf, g >> 1 & 1);
+                    wait(C::BAR_V_FULL, g & 1);
+                    wait(C::BAR_V_FULL + 1, g & 1);
                     if (half == 0 && *reinterpret_cast<const uint32_t *>(smem + C::OFF_FLAGS + (g & 3) * 4)) {
-                        const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + g % 3 * C::NAN_BYTES);
+                        const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + (g & 1) * C::NAN_BYTES);
 #pragma unroll 1
                         for (int k = 0; k < TILE; ++k)
                             if (pos0 + k >= lo && pos0 + k < hi)
@@ -556,32 +567,32 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // this thread's scores, 16 at a time; those that the row does not see are -inf
                 auto for_groups = [&](auto f) {
                     uint32_t r[2][CHUNK];
-                    tmem_ld(s_addr + half * (TILE / 2), r[0]);
-                    tmem_ld(s_addr + half * (TILE / 2) + CHUNK, r[1]);
-                    tmem_wait_ld();
-                    tmem_pin(r[0]);
-                    tmem_pin(r[1]);
+                    tmem_ld(s_addr + half * C::HALF, r[0]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 scales = info[half * 2 + i];
+                    for (int i = 0; i < GROUPS / 2; ++i) {
+                        tmem_wait_ld();
+                        tmem_pin(r[i & 1]);
+                        if (i + 1 < GROUPS / 2)
+                            tmem_ld(s_addr + half * C::HALF + (i + 1) * CHUNK, r[(i + 1) & 1]);
+                        const float4 scales = info[half * (GROUPS / 2) + i];
                         if (!whole) {
                             const uint32_t word = __float_as_uint(scales.w);
                             const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
-                            const int key0 = pos0 + half * (TILE / 2) + i * CHUNK;
+                            const int key0 = pos0 + half * C::HALF + i * CHUNK;
 #pragma unroll
                             for (int k = 0; k < CHUNK; ++k) {
                                 const bool see = page && key0 + k >= lo && key0 + k < hi;
-                                r[i][k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[i][k];
+                                r[i & 1][k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[i & 1][k];
                             }
                         }
                         // (not 0: a hidden score is -inf * c)
-                        f(i, r[i], fmaxf(scale_row * scales.x, 1.17549435e-38f), scales.y, scales.z);
+                        f(i, r[i & 1], fmaxf(scale_row * scales.x, 1.17549435e-38f), scales.y, scales.z);
                     }
                 };
                 // Weights as f16 pairs, by the maximum so far.  Their sum tells whether one is
                 // too large for it: only then (and for a row's first keys) is the tile's maximum
                 // taken, O and l brought to it, and the weights taken again.
-                uint32_t p[16];
+                uint32_t p[32];
                 float sum, add_l;
                 bool waited = j == 0;
                 bool again = __any_sync(0xffffffffu, M == -INFINITY && lo < pos0 + TILE && hi > pos0);
@@ -643,7 +654,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         sum += sum0 + sum1;
                         add_l = fmaf(sum0 + sum1, lf, add_l);
                     });
-                    // (f16 ends at 65504; by the tile's own maximum the sum is 2^11 at most.)  The
+                    // (f16 ends at 65504; by the tile's own maximum the sum is 2^12 at most.)  The
                     // weights go over the scores, so both threads have read theirs after this.
                     again = pair_any(sum > 32768.f);
                     if (!again)
@@ -655,7 +666,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // complete.
                 if (!waited && j == n - 1)
                     wait(C::BAR_O_DONE, (g - 1) & 1);
-                tmem_st16(s_addr + half * 16, p);
+                tmem_st32(s_addr + half * 32, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(C::BAR_P_FULL + buf);
@@ -763,7 +774,7 @@ fa2_status launch_chunk(const AttnArgs &a)
     const int grid = line_grid<C>(a, parts.data != nullptr);
     const EncodeTiled encode = encode_tiled();
     CUtensorMap k_map, v_map;
-    const int rows = a.c.page_shift < 6 ? 1 << a.c.page_shift : C::TILE;
+    const int rows = 1 << a.c.page_shift;
     if (!encode || !page_map(encode, &k_map, a.c.k, a.c, C::D, rows, C::ROW) ||
         !page_map(encode, &v_map, a.c.v, a.c, C::D, rows, C::ROW))
         return FA2_ERR_CUDA;
