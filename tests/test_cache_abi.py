@@ -40,13 +40,26 @@ def test_library_exports_what_its_header_declares(lib):
         assert exported == header_functions()
 
 
+class Cache(ctypes.Structure):
+    """struct fa2_cache, the stride arrays as single fields."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")] +
+                [(n, ctypes.c_longlong) for n in ("k_page", "k_head", "k_slot", "v_page", "v_head", "v_slot")] +
+                [(n, ctypes.c_int) for n in ("num_pages", "H", "page_size", "D", "B", "max_pages")])
+
+
 def cache(lib, **kw):
     f = dict(k=P, v=P, k_scale=P, v_scale=P, page_table=P, num_pages=4, H=2, page_size=16, D=64, B=1, max_pages=2)
     f.update(kw)
-    return lib._Cache(**f)
+    return bytes(Cache(**f))
 
 
-ll3 = ctypes.c_longlong * 3
+def ll3(*x):
+    return bytes((ctypes.c_longlong * 3)(*x))
+
+
+def test_the_binding_packs_the_structure(lib):
+    c = Cache(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16, 17)
+    assert bytes(c) == lib._pack_cache(*range(1, 18))
 
 
 def write(lib, c, k=P, v=P, ks=None, vs=None, starts=P, counts=None, L=5, f="fa2_cache_write"):
