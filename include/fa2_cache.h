@@ -140,6 +140,9 @@ fa2_status fa2_cache_read(const fa2_cache *c, void *k, void *v, const long long 
  *              work.  Calls that may run at the same time must not share one.
  *
  * Results do not depend on timing: the parts of a row are merged in a fixed order.
+ * The work of a call is counted in tiles of 128 keys by blocks of 8 to 128 of a
+ * key/value head's Lq * Hq / H rows; sizes for which max_pages full pages would
+ * make 2^31 of them or more are refused (FA2_ERR_UNSUPPORTED).
  * Errors as fa2_cache_write, also FA2_ERR_INVALID_ARG for a bad scale or window, Hq
  * not a multiple of H, or a workspace that is misaligned or too small.
  */

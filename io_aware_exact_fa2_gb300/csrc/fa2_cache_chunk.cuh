@@ -43,7 +43,7 @@ struct ChunkCfg {
     static constexpr int D = D_;
     static constexpr int R = 128;                    // query rows of a unit
     static constexpr int TILE = 128;                 // keys
-    static constexpr int UNIT_COST = 2, MIN_TILES = 2;   // see fa2_cache_line.cuh
+    static constexpr int UNIT_COST = 4, MIN_TILES = 2;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = TILE;               // a tile begins at a multiple
     static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
     static constexpr int WARP_CONVERT = 8, WARP_MMA = 12, WARP_LOAD = 13;
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     // registers in their loops over tiles.
     __shared__ struct {
         Range range;
-        long long first, end;
+        int first, end;
         Line<C> line[C::T / 32];
     } sh;
 
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     const int cta = blockIdx.x;
     {
         Range range;
-        long long first, end;
+        int first, end;
         Line<C> line;
         if (!find_range<C>(a, cut, sh_line, range, first, end, line))
             return;
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     };
     // the tiles of the unit `line` that lie in this CTA's range
     auto part_of = [&](int &tile0, int &tile1) {
-        tile0 = cut && sh.first > line.at ? static_cast<int>(sh.first - line.at) : 0;
-        tile1 = cut && sh.end < line.at + line.span.tiles ? static_cast<int>(sh.end - line.at) : line.span.tiles;
+        tile0 = cut && sh.first > line.at ? sh.first - line.at : 0;
+        tile1 = cut && sh.end < line.at + line.span.tiles ? sh.end - line.at : line.span.tiles;
     };
     auto next_unit = [&]() -> bool {     // by a whole warp
         __syncwarp();
@@ -772,6 +772,8 @@ fa2_status launch_chunk(const AttnArgs &a)
     if (!parts_of<C>(a, parts))
         return FA2_ERR_INVALID_ARG;
     const int grid = line_grid<C>(a, parts.data != nullptr);
+    if (grid == 0)
+        return FA2_ERR_UNSUPPORTED;
     const EncodeTiled encode = encode_tiled();
     CUtensorMap k_map, v_map;
     const int rows = 1 << a.c.page_shift;

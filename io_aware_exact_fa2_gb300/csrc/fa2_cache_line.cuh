@@ -10,6 +10,8 @@
 // Lengths are device data, so every CTA lays out the line for itself.
 #pragma once
 
+#include <climits>
+
 #include "fa2_cache.cuh"
 #include "sm103_ptx.cuh"
 
@@ -51,18 +53,18 @@ bool parts_of(const AttnArgs &a, Parts &parts)
     return true;
 }
 
-// CTAs to launch: no more than the longest sequences could make ranges for.
+// CTAs to launch: no more than the longest sequences could make ranges for; 0 if the line
+// could be longer than an int can count.
 template <class C>
 int line_grid(const AttnArgs &a, bool cut)
 {
     const long long most = a.num_sms * C::CTAS;
     const long long blocks = (static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R;
-    const long long tiles = ((static_cast<long long>(a.c.max_pages) << a.c.page_shift) + C::TILE - 1) / C::TILE + 1;
-    long long grid = cut ? (tiles + C::UNIT_COST + C::MIN_TILES - 1) / C::MIN_TILES : 1;
-    grid = grid > most ? most : grid;
-    grid *= blocks > most ? most : blocks;
-    grid = grid > most ? most : grid;
-    grid *= static_cast<long long>(a.c.B) * a.c.H;
+    const long long length = ((static_cast<long long>(a.c.max_pages) << a.c.page_shift) + C::TILE - 1) / C::TILE + 1 + C::UNIT_COST;
+    const long long units = static_cast<long long>(a.c.B) * a.c.H * blocks;   // (B H, blocks < 2^31)
+    if (units > INT_MAX || units * length > INT_MAX)
+        return 0;
+    const long long grid = cut ? (units * length + C::MIN_TILES - 1) / C::MIN_TILES : units;
     return static_cast<int>(grid > most ? most : grid);
 }
 
@@ -114,27 +116,24 @@ __device__ __forceinline__ int row_blocks(const AttnArgs &a, const Seq &s)
     return (s.n * a.G + C::R - 1) / C::R;
 }
 
-// x / y, both >= 0 and y > 0: 32-bit operands, the usual ones, divide several times faster.
-__device__ __forceinline__ long long divide(long long x, long long y)
-{
-    if (((x | y) >> 32) == 0)
-        return static_cast<unsigned>(x) / static_cast<unsigned>(y);
-    return x / y;
-}
-
-// One CTA's share of the line of tiles.
+// The line cut into `grid` ranges, the first `more` of them of size + 1 tiles.
 struct Range {
-    long long total;    // the line's length
-    int grid;           // ranges
-    __device__ long long begin(int c) const { return divide(total * c, grid); }
+    int grid, size, more;
+    __device__ Range() = default;
+    __device__ Range(int total, int ranges) : grid(ranges), size(total / ranges), more(total - total / ranges * ranges) {}
+    __device__ int begin(int c) const { return c * size + (c < more ? c : more); }
     // the range that tile x lies in
-    __device__ int owner(long long x) const { return static_cast<int>(divide((x + 1) * grid + total - 1, total) - 1); }
+    __device__ int owner(int x) const
+    {
+        const int y = x - more * (size + 1);
+        return y < 0 ? x / (size + 1) : more + y / size;
+    }
 };
 
 // A unit's place on the line.
 template <class C>
 struct Line {
-    long long at;      // its first tile
+    int at;            // its first tile
     int b, h, rb;
     Seq s;
     Span span;
@@ -169,56 +168,52 @@ struct Line {
 };
 
 struct LineShared {
-    long long scan[32], at;
-    int b, rb, kv, n;
+    int scan[32], at, b, rb, kv, n;
 };
 
 // Lays out the line and finds this CTA's range of it, [first, end), and the unit it
 // begins with; all C::T threads call it.  False: nothing to do.  Uncut (cut false), a
 // unit belongs whole to the range that its first tile lies in.
 template <class C>
-__device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShared &sh, Range &range, long long &first,
-                                           long long &end, Line<C> &line)
+__device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShared &sh, Range &range, int &first, int &end,
+                                           Line<C> &line)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // A thread takes a run of the row blocks (as many a sequence as Lq can have), and the
     // one whose run holds the first tile finds its unit.
-    const int blocks = static_cast<int>((static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R);
-    const long long items = static_cast<long long>(a.c.B) * blocks;
-    const int per = static_cast<int>(divide(items + C::T - 1, C::T));
-    const long long i0 = static_cast<long long>(tid) * per, i1 = i0 + per < items ? i0 + per : items;
-    const int b0 = blocks == 1 ? static_cast<int>(i0) : static_cast<int>(divide(i0, blocks));
-    const int rb0 = static_cast<int>(i0 - static_cast<long long>(b0) * blocks);
-    // calls f(b, rb, sequence, the heads' length) for each of them until it returns true
-    auto walk = [&](auto f) {
-        int b = b0, rb = rb0;
-        Seq s{0, 0};
-        if (i0 < i1)
+    const int blocks = (a.Lq * a.G + C::R - 1) / C::R, items = a.c.B * blocks;
+    const int per = items <= C::T ? 1 : (items + C::T - 1) / C::T;
+    const int i0 = tid * per, i1 = i0 + per < items ? i0 + per : items;
+    const int b0 = blocks == 1 ? i0 : i0 / blocks, rb0 = i0 - b0 * blocks;
+    Seq s{0, 0};
+    int length = 0;                     // of the block's units on the line, all heads'
+    auto item = [&](int b, int rb, bool read) {
+        if (read)
             s = sequence(a, b);
-        for (long long i = i0; i < i1; ++i) {
-            if (rb * C::R < s.n * a.G && f(b, rb, s, (span_of<C>(a, s, rb).tiles + C::UNIT_COST) * static_cast<long long>(a.c.H)))
-                return;
-            if (++rb == blocks && i + 1 < i1) {
+        length = rb * C::R < s.n * a.G ? (span_of<C>(a, s, rb).tiles + C::UNIT_COST) * a.c.H : 0;
+    };
+    int mine = 0;
+    {
+        int b = b0, rb = rb0;
+        for (int i = i0; i < i1; ++i) {
+            item(b, rb, i == i0 || rb == 0);
+            mine += length;
+            if (++rb == blocks) {
                 rb = 0;
-                s = sequence(a, ++b);
+                ++b;
             }
         }
-    };
-    long long mine = 0;
-    walk([&](int, int, const Seq &, long long n) {
-        mine += n;
-        return false;
-    });
-    long long upto = mine;
+    }
+    int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+        const int x = __shfl_up_sync(0xffffffffu, upto, d);
         upto += lane >= d ? x : 0;
     }
     if (lane == 31)
         sh.scan[warp] = upto;
     __syncthreads();
-    long long before = 0, total = 0;
+    int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < C::T / 32; ++w) {
         before += w < warp ? sh.scan[w] : 0;
@@ -227,39 +222,40 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     before += upto - mine;
     if (total == 0)
         return false;
-    range.total = total;
-    const long long most = cut ? divide(total + C::MIN_TILES - 1, C::MIN_TILES) : total;
-    range.grid = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    const int most = cut ? (total + C::MIN_TILES - 1) / C::MIN_TILES : total;
+    range = Range(total, most < static_cast<int>(gridDim.x) ? most : static_cast<int>(gridDim.x));
     const int cta = blockIdx.x;
     if (cta >= range.grid)
         return false;
     first = range.begin(cta);
     end = range.begin(cta + 1);
-    if (first >= end)
-        return false;
     if (first >= before && first < before + mine) {
-        long long at = before;
-        walk([&](int b, int rb, const Seq &s, long long n) {
-            if (first >= at + n) {
-                at += n;
-                return false;
+        int b = b0, rb = rb0, at = before;
+        if (per > 1) {
+            item(b, rb, true);
+            while (first >= at + length) {
+                at += length;
+                if (++rb == blocks) {
+                    rb = 0;
+                    ++b;
+                }
+                item(b, rb, rb == 0);
             }
-            sh.at = at;
-            sh.b = b;
-            sh.rb = rb;
-            sh.kv = s.kv;
-            sh.n = s.n;
-            return true;
-        });
+        }
+        sh.at = at;
+        sh.b = b;
+        sh.rb = rb;
+        sh.kv = s.kv;
+        sh.n = s.n;
     }
     __syncthreads();
     line.b = sh.b;
     line.rb = sh.rb;
     line.s = Seq{sh.kv, sh.n};
     line.span = span_of<C>(a, line.s, line.rb);
-    const int length = line.span.tiles + C::UNIT_COST;
-    line.h = static_cast<int>(divide(first - sh.at, length));
-    line.at = sh.at + static_cast<long long>(line.h) * length;
+    const int unit = line.span.tiles + C::UNIT_COST;
+    line.h = (first - sh.at) / unit;
+    line.at = sh.at + line.h * unit;
     // (the range may begin in a unit's extra length: then with the next unit)
     if ((line.at + line.span.tiles <= first || (!cut && line.at < first)) && !line.next(a))
         return false;

@@ -46,7 +46,7 @@ struct StepCfg {
     static constexpr int D = D_;
     static constexpr int R = R_;                     // query rows of a unit
     static constexpr int TILE = 128;                 // keys
-    static constexpr int UNIT_COST = 2, MIN_TILES = 2;   // see fa2_cache_line.cuh
+    static constexpr int UNIT_COST = 3, MIN_TILES = 1;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = 128;                // whole pages: a tile begins at a multiple
     static constexpr int CTAS = D == 64 ? (R == 8 ? 3 : 2) : D == 128 ? 2 : 1;   // an SM
     static constexpr int WARP_LOAD = 4, WARP_MMA = 5;
@@ -110,28 +110,35 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool cut = parts.data != nullptr;
     const int cta = blockIdx.x;
-    Range range;
-    long long first, end;
-    Line<C> line;
-    if (!find_range<C>(a, cut, sh_line, range, first, end, line))
-        return;
-
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *const smem = smem_raw + (base - smem_u32(smem_raw));
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
-    if (tid == 0) {
-        for (int i = 0; i < C::NUM_BAR; ++i)
-            mbar_init(bar(i), i == C::BAR_Q_FULL || i == C::BAR_P_FULL ? 4 : 1);
-        fence_mbar_init();
-    }
+    volatile uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    // (while the lengths are on their way)
     if (warp == C::WARP_MMA) {
         tmem_alloc(base + C::OFF_MISC, C::TMEM_COLS);
         tmem_relinquish();
+    } else if (tid == 32 * C::WARP_LOAD) {
+        for (int i = 0; i < C::NUM_BAR; ++i)
+            mbar_init(bar(i), i == C::BAR_Q_FULL || i == C::BAR_P_FULL ? 4 : 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&k_map);
+        tma_prefetch_desc(&v_map);
     }
     tc_fence_before();
-    __syncthreads();
+    Range range;
+    int first, end;
+    Line<C> line;
+    const bool any = find_range<C>(a, cut, sh_line, range, first, end, line);   // (barriers of the CTA in it)
+    if (!any) {
+        if (warp == C::WARP_MMA) {
+            __syncwarp();
+            tmem_dealloc(*tmem_slot, C::TMEM_COLS);
+        }
+        return;
+    }
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::OFF_MISC);
+    const uint32_t tmem = *tmem_slot;
 
     // A wait that ran out is recorded and not waited for again: the role runs on to its end
     // without waiting (its outputs are undefined), so that barriers between warps still match.
@@ -147,8 +154,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     };
     // the tiles of the unit `line` that lie in this CTA's range
     auto part_of = [&](int &tile0, int &tile1) {
-        tile0 = cut && first > line.at ? static_cast<int>(first - line.at) : 0;
-        tile1 = cut && end < line.at + line.span.tiles ? static_cast<int>(end - line.at) : line.span.tiles;
+        tile0 = cut && first > line.at ? first - line.at : 0;
+        tile1 = cut && end < line.at + line.span.tiles ? end - line.at : line.span.tiles;
     };
     auto next_unit = [&]() { return line.next(a) && line.at < end; };
     uint32_t *const sh_info = reinterpret_cast<uint32_t *>(smem + C::OFF_INFO);   // [4][8 groups of 16 keys]
@@ -160,10 +167,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         const int pages = TILE >> a.c.page_shift;          // of a tile: one a lane
         const uint32_t page_bytes = static_cast<uint32_t>(D) << a.c.page_shift;
         const uint32_t offset = static_cast<uint32_t>(lane) * C::ROW << a.c.page_shift;   // in each panel
-        if (lane == 0) {
-            tma_prefetch_desc(&k_map);
-            tma_prefetch_desc(&v_map);
-        }
         uint32_t issued = 0;                               // items
         do {
             int tile0, tile1;
@@ -190,25 +193,26 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * page_bytes;
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
-                    const uint32_t item = 2 * (it + j) + side, slot = item % SLOTS;
+                    const uint32_t item = 2 * (it + j) + side, slot = item % SLOTS, full = bar(C::BAR_FULL + slot);
                     if (item >= SLOTS)
                         warp_wait(C::BAR_EMPTY + slot, (item / SLOTS - 1) & 1, STEP_ERR_LOAD);
                     if (!ok)
                         break;
-                    // (the tile four back has been through its softmax: its values' slot came
-                    // back before the last tile was loaded)
-                    if (side == 0 && lane < pages)
-                        for (int k = 0; k < 1 << (a.c.page_shift - 4); ++k)
-                            sh_info[((it + j) & 3) * (TILE / CHUNK) + (lane << (a.c.page_shift - 4)) + k] = sc;
-                    __syncwarp();
                     if (lane == 0)
-                        mbar_arrive_expect_tx(bar(C::BAR_FULL + slot), bytes);
+                        expect_tx(full, bytes);
                     __syncwarp();
                     if (id >= 0)
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p)
                             tma_load_4d(base + C::OFF_RING + slot * C::SLOT + p * C::PANEL + offset, side ? &v_map : &k_map,
-                                        p * 128, 0, h, id, bar(C::BAR_FULL + slot));
+                                        p * 128, 0, h, id, full);
+                    // The keys' copies are under way while the scales arrive.  (Whose place the
+                    // tile four back had: it has been through its softmax, for its values' slot
+                    // came back before the last tile was loaded.)
+                    if (side == 0 && lane < pages)
+                        for (int k = 0; k < 1 << (a.c.page_shift - 4); ++k)
+                            sh_info[((it + j) & 3) * (TILE / CHUNK) + (lane << (a.c.page_shift - 4)) + k] = sc;
+                    warp_arrive(C::BAR_FULL + slot);
                     issued = item + 1;
                 }
                 id = id_next;
@@ -663,6 +667,8 @@ fa2_status launch_step(const AttnArgs &a)
     if (!parts_of<C>(a, parts))
         return FA2_ERR_INVALID_ARG;
     const int grid = line_grid<C>(a, parts.data != nullptr);
+    if (grid == 0)
+        return FA2_ERR_UNSUPPORTED;
     const EncodeTiled encode = encode_tiled();
     CUtensorMap k_map, v_map;
     const int rows = 1 << a.c.page_shift;

@@ -59,6 +59,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, int *e
     return true;
 }
 
+// `bytes` more to come in an mbarrier's present phase, which an arrival has to follow.
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // N consecutive 32-bit columns of this warp's 32 tensor-memory lanes; valid after the wait.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4])
 {

@@ -466,6 +466,20 @@ def test_on_another_stream():
     ref.check_attention(o.cpu(), lse.cpu(), want)
 
 
+def test_more_work_than_can_be_counted_is_refused():
+    """A table for 2^30 positions and 2^15 query rows: 2^31 tiles and more."""
+    c = Cache(1, 1, 64, 16, [40], seed=17)
+    dev = list(c.device())
+    dev[4] = torch.full((1, 1 << 26), -1, dtype=torch.int32, device=DEV)
+    q = torch.zeros(1, 1, 1 << 15, 64, dtype=torch.bfloat16, device=DEV)
+    o, lse = torch.zeros_like(q), torch.zeros(1, 1, 1 << 15, device=DEV)
+    with pytest.raises(RuntimeError, match="FA2_ERR_UNSUPPORTED"):
+        fa2().fa2_cache_attn(q, *dev, i32([40]), o, lse)
+    # the same table with a row: every page is missing
+    fa2().fa2_cache_attn(q[:, :, :1].contiguous(), *dev, i32([1 << 30]), o[:, :, :1].contiguous(), lse[:, :, :1].contiguous())
+    assert fa2().fa2_cache_get_device_error() == (0, 0)
+
+
 def test_a_small_workspace_is_refused():
     c = Cache(1, 1, 64, 16, [40], seed=16)
     dev = c.device()
