@@ -24,6 +24,13 @@ __device__ __forceinline__ void load16(Row16 &r, const uint16_t *p)
     r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
 }
 
+// Largest magnitudes of two packed bf16 (a NaN only where there is nothing else).
+__device__ __forceinline__ uint32_t packed_max(uint32_t m, uint32_t w)
+{
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w & 0x7fff7fffu));
+    return m;
+}
+
 // Largest finite magnitude among two packed bf16, as bf16 bits (magnitudes of bf16
 // order as their bits do).
 __device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t w)
@@ -43,13 +50,25 @@ __device__ __forceinline__ int least_exponent(uint32_t a)
     return e < kMinExponent ? kMinExponent : e > kMaxExponent ? kMaxExponent : e;
 }
 
-// x * inv with infinities as NaN: the saturating conversion below would make them 448.
-__device__ __forceinline__ float scaled(float x, float inv) { return fmaf(x, inv, x * 0.f); }
+// x * inv; with INF, infinities as NaN: the saturating conversion below would make them 448.
+template <bool INF>
+__device__ __forceinline__ float scaled(float x, float inv)
+{
+    return INF ? fmaf(x, inv, x * 0.f) : x * inv;
+}
 
+template <bool INF>
 __device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, float inv)
 {
-    return ptx::pack_e4m3x4(scaled(__uint_as_float(a << 16), inv), scaled(__uint_as_float(a & 0xffff0000u), inv),
-                            scaled(__uint_as_float(b << 16), inv), scaled(__uint_as_float(b & 0xffff0000u), inv));
+    return ptx::pack_e4m3x4(scaled<INF>(__uint_as_float(a << 16), inv), scaled<INF>(__uint_as_float(a & 0xffff0000u), inv),
+                            scaled<INF>(__uint_as_float(b << 16), inv), scaled<INF>(__uint_as_float(b & 0xffff0000u), inv));
+}
+
+template <bool INF>
+__device__ __forceinline__ uint4 quantise16(const Row16 &r, float inv)
+{
+    return make_uint4(quantise4<INF>(r.w[0], r.w[1], inv), quantise4<INF>(r.w[2], r.w[3], inv),
+                      quantise4<INF>(r.w[4], r.w[5], inv), quantise4<INF>(r.w[6], r.w[7], inv));
 }
 
 // Four codes brought from one scale to a larger one (f = 2^(before - after)).
@@ -109,12 +128,26 @@ __global__ void __launch_bounds__(T) write_kernel(const MoveArgs a, const int to
             load16(r[k], x + (p0 + s - start) * a.sl[side]);
     }
     const int before = s0 > 0 ? static_cast<int>(*scale) - 127 : INT_MIN;
+    // The arithmetic counts here: the plain maximum, and only where it is no finite number
+    // (an infinity among them, or nothing but NaN) that of the finite ones.
+    uint32_t pair = 0;
 #pragma unroll
     for (int k = 0; k < NP; ++k)
         if (s0 + row0 + k * step < s1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                m = finite_max(m, r[k].w[i]);
+                pair = packed_max(pair, r[k].w[i]);
+    m = max(pair & 0xffffu, pair >> 16);
+    const bool odd = m >= 0x7f80u;
+    if (odd) {
+        m = 0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+            if (s0 + row0 + k * step < s1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    m = finite_max(m, r[k].w[i]);
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     if (T > 32) {
         __shared__ uint32_t part[T / 32];
@@ -132,12 +165,7 @@ __global__ void __launch_bounds__(T) write_kernel(const MoveArgs a, const int to
     for (int k = 0; k < NP; ++k) {
         const int s = s0 + row0 + k * step;
         if (s < s1) {
-            uint4 w;
-            w.x = quantise4(r[k].w[0], r[k].w[1], inv);
-            w.y = quantise4(r[k].w[2], r[k].w[3], inv);
-            w.z = quantise4(r[k].w[4], r[k].w[5], inv);
-            w.w = quantise4(r[k].w[6], r[k].w[7], inv);
-            *reinterpret_cast<uint4 *>(codes + s * half.s_slot) = w;
+            *reinterpret_cast<uint4 *>(codes + s * half.s_slot) = odd ? quantise16<true>(r[k], inv) : quantise16<false>(r[k], inv);
         }
     }
     if (s0 > 0 && e > before) {
@@ -166,7 +194,7 @@ fa2_status run_write(const MoveArgs &a, long long blocks, int touched, int lpr_s
 }
 
 constexpr int READ_T = 256;      // threads a block
-constexpr int READ_ROWS = 4;     // rows a thread
+constexpr int READ_ROWS = 2;     // rows a thread (of 805 MB: 1 row 128 us, 2 122, 4 138, 8 171)
 
 // A block copies READ_ROWS * 16 / D * READ_T rows of one head, keys or values.
 __global__ void __launch_bounds__(READ_T) read_kernel(const MoveArgs a, const int chunks, const int lpr_shift)
