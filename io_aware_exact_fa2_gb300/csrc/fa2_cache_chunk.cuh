@@ -18,16 +18,16 @@
 //
 // What bounds it.  4 D operations a (row, key) pair against D / 64 cache bytes a row and
 // key: the tensor pipe.  (Two e4m3 products take the time of one of f16, and K needs no
-// conversion.)  128 rows x 64 keys x D = 128 take some 540 cycles; the exponentials and the
-// rest of the softmax cost about as much issue time.  So the work has warps of its own,
-//     8 warps   softmax: two threads a row, each half of a tile's keys; S from and P to
-//               tensor memory
-//     4 warps   values' codes to f16 operands in shared memory (swizzled)
-//     1 warp    issues the products
-//     1 warp    pages into shared memory by TMA
-// and at D <= 128 two CTAs share an SM (256 columns of tensor memory each), so that one's
-// exponentials run under the other's products.  Work is cut and merged as in
-// fa2_cache_line.cuh.
+// conversion.)  128 rows x 128 keys x D = 128 take some 1100 cycles of it; the exponentials
+// and the rest of the softmax cost about as much issue time, and V's conversion is shared by
+// the 256 rows of a unit (128 at D = 256, where tensor memory holds no more).  So the work
+// has warps of its own,
+//     8 or 16 warps  softmax: two threads a row, each half of a tile's keys; S from and P to
+//                    tensor memory
+//     4 warps        values' codes to f16 operands in shared memory (swizzled)
+//     1 warp         issues the products: one 128-row tile's run under the other's softmax
+//     1 warp         pages into shared memory by TMA
+// on one CTA an SM.  Work is cut and merged as in fa2_cache_line.cuh.
 #pragma once
 
 #include <atomic>
@@ -41,53 +41,54 @@ namespace cache {
 template <int D_>
 struct ChunkCfg {
     static constexpr int D = D_;
-    static constexpr int R = 128;                    // query rows of a unit
+    static constexpr int NQ = D == 256 ? 1 : 2;      // 128-row tiles of a unit
+    static constexpr int R = 128 * NQ;               // its query rows
     static constexpr int TILE = 128;                 // keys
-    static constexpr int UNIT_COST = 4, MIN_TILES = 2;   // see fa2_cache_line.cuh
+    static constexpr int UNIT_COST = 3, MIN_TILES = 2;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = TILE;               // a tile begins at a multiple
-    static constexpr int CTAS = D <= 128 ? 2 : 1;    // an SM
-    static constexpr int WARP_CONVERT = 8, WARP_MMA = 12, WARP_LOAD = 13;
-    static constexpr int T = 32 * 16;                // (the last warpgroup: two idle warps)
-    // With two CTAs an SM the launch leaves 64 registers a thread, 256 for the four
-    // warpgroups' lanes together: the softmax rises, the others give.
-    static constexpr bool REG_SPLIT = CTAS == 2;
-    static constexpr int REG_SOFTMAX = 88, REG_CONVERT = 40, REG_ISSUE = 40;
-    static_assert(2 * REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 4 * 64, "the split draws on the launch's registers");
+    static constexpr int CTAS = 1;                   // an SM
+    static constexpr int WARP_CONVERT = 8 * NQ, WARP_MMA = WARP_CONVERT + 4, WARP_LOAD = WARP_MMA + 1;
+    static constexpr int T = 32 * (WARP_MMA + 4);    // (the last warpgroup: two idle warps)
+    // With six warpgroups the launch leaves 80 registers a thread, 480 for the warpgroups'
+    // lanes together: the softmax rises, the others give.
+    static constexpr bool REG_SPLIT = NQ == 2;
+    static constexpr int REG_SOFTMAX = 88, REG_CONVERT = 64, REG_ISSUE = 64;
+    static_assert(4 * REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 6 * 80, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
     static constexpr int ROW = D == 64 ? 64 : 128;   // bytes of a row of codes: its swizzle span
     static constexpr int PANELS = D / ROW, PANEL = TILE * ROW;       // of a stage of codes
-    static constexpr int STAGE = TILE * D, KS = D == 64 ? 2 : 1, VS = D == 64 ? 2 : 1;   // stages of keys, of values
-    static constexpr int SB = D == 256 ? 2 : 1;                      // buffers of S
-    static constexpr int Q_PANEL = R * ROW, Q_TERM = R * D;          // Q: two terms of codes
-    // V in f16, each half of a tile's keys a buffer: panels of 64 columns, 128-byte rows
-    static constexpr int HALF = TILE / 2, V_PANEL = HALF * 128, V_BYTES = HALF * D * 2;
-    static constexpr int OFF_Q = 0, OFF_V = 2 * Q_TERM, OFF_K = OFF_V + 2 * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
-    // Rings of tiles: group scales, NaN flags, NaN values by key.  (A tile is loaded, and the
-    // one after it converted, when the one two back has been through its softmax.)
+    static constexpr int STAGE = TILE * D, KS = D == 256 ? 1 : 2, VS = D == 256 ? 1 : 2;   // stages of keys, of values
+    static constexpr int Q_PANEL = 128 * ROW, Q_TERM = 128 * D, Q_TILE = 2 * Q_TERM;   // Q: two terms of codes a row tile
+    // V in f16, half a tile's keys a buffer: panels of 64 columns, 128-byte rows
+    static constexpr int HALF = TILE / 2, V_PANEL = HALF * 128, V_BYTES = HALF * D * 2, VB = D == 256 ? 2 : 4;
+    static constexpr int OFF_Q = 0, OFF_V = NQ * Q_TILE, OFF_K = OFF_V + VB * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
+    // Rings of four tiles: group scales, NaN flags, NaN values by key.  (Tile g is loaded when
+    // the values of g - VS have been read, which waits for the products of g - VS - VB / 2.)
     static constexpr int NAN_WORDS = D / 32;
     static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16;
     static constexpr int OFF_FLAGS = OFF_INFO + 4 * INFO_BYTES;
     static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
-    static constexpr int OFF_MARK = OFF_NAN + 2 * NAN_BYTES;         // values of O that are NaN, by row
+    static constexpr int OFF_MARK = OFF_NAN + 4 * NAN_BYTES;         // values of O that are NaN, by row
     static constexpr int OFF_PAIR = OFF_MARK + R * NAN_WORDS * 4;    // a float of each softmax thread
     static constexpr int OFF_BAR = OFF_PAIR + 2 * R * 4;
-    static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_V_FULL = 2, BAR_V_EMPTY = 4, BAR_S_FULL = 6, BAR_P_FULL = 8,
-                         BAR_O_DONE = 10, BAR_O_FREE = 11, BAR_GROUP = 12, BAR_DRAIN = 13, BAR_K_FULL = 14,
+    // (the first six: one for each row tile)
+    static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 2, BAR_S_FULL = 4, BAR_P_FULL = 6, BAR_O_DONE = 8, BAR_O_FREE = 10,
+                         BAR_DRAIN = 12, BAR_V_FULL = 13, BAR_V_EMPTY = BAR_V_FULL + VB, BAR_K_FULL = BAR_V_EMPTY + VB,
                          BAR_K_EMPTY = BAR_K_FULL + KS, BAR_RAW_FULL = BAR_K_EMPTY + KS, BAR_RAW_EMPTY = BAR_RAW_FULL + VS,
                          NUM_BAR = BAR_RAW_EMPTY + VS;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // 1024: operand alignment
+    static_assert(VS + VB / 2 <= 4, "the rings hold the tiles under way");
 
-    static constexpr int TM_S = 0, TM_O = SB * TILE;
-    static constexpr int TMEM_COLS = D <= 128 ? 256 : 512;
-
+    static constexpr int TM_S = 0, TM_O = NQ * TILE;
+    static constexpr int TMEM_COLS = 512;
     // kind::f16 with f16 A and B (formats 0), fp32 accumulator
     static constexpr uint32_t idesc(int n, bool b_mn)
     {
-        return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(R >> 4) << 24);
+        return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
     }
-    static_assert(CTAS * (SMEM_BYTES + 1024 + 512) <= 228 * 1024 && CTAS * TMEM_COLS <= 512 && SB * TILE + D <= TMEM_COLS, "an SM holds CTAS of them");
+    static_assert(SMEM_BYTES + 1024 + 1024 <= 228 * 1024 && NQ * (TILE + D) <= TMEM_COLS, "an SM holds it");
 };
 
 // Error codes of waits that ran out (bits 8-11 the waiting role).
@@ -154,9 +155,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
     if (tid == 0) {
         for (int i = 0; i < C::NUM_BAR; ++i) {
-            const bool softmax = i == C::BAR_Q_FULL || i / 2 == C::BAR_P_FULL / 2 || i == C::BAR_O_FREE || i == C::BAR_GROUP;
-            const bool convert = i / 2 == C::BAR_V_FULL / 2 || i >= C::BAR_RAW_EMPTY;
-            mbar_init(bar(i), softmax ? 8 : convert ? 4 : 1);
+            const bool rows = i / 2 == C::BAR_Q_FULL / 2 || i / 2 == C::BAR_P_FULL / 2 || i / 2 == C::BAR_O_FREE / 2;
+            const bool convert = (i >= C::BAR_V_FULL && i < C::BAR_V_EMPTY) || i >= C::BAR_RAW_EMPTY;
+            mbar_init(bar(i), rows ? 8 : convert ? 4 : 1);
         }
         fence_mbar_init();
     }
@@ -197,89 +198,115 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     auto is_whole = [](const uint8_t *smem, uint32_t g) {
         return *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES + GROUPS * 16) != 0;
     };
-    uint32_t it = 0;       // tiles before the present unit's first: buffers alternate by tile
-    uint32_t unit = 0;
+    uint32_t it = 0;               // tiles before the present unit's first
+    auto row_tiles = [&] { return C::NQ > 1 && line.s.n * a.G - line.rb * R > 128 ? 2 : 1; };
 
     if (warp >= C::WARP_MMA) {
         // ============================================ one thread issues the products
         if constexpr (C::REG_SPLIT)
             setmaxnreg_dec<C::REG_ISSUE>();
         if (warp == C::WARP_MMA) {
-            // (all lanes wait: a lone lane would have to poll)
-            const bool leader = elect_one();
-            const uint64_t desc_q = D == 64 ? sdesc_sw64(base + C::OFF_Q, 16, 512) : sdesc_sw128(base + C::OFF_Q, 16, 1024);
-            const uint64_t desc_k = D == 64 ? sdesc_sw64(base + C::OFF_K, 16, 512) : sdesc_sw128(base + C::OFF_K, 16, 1024);
-            const uint64_t desc_v = sdesc_sw128(base + C::OFF_V, C::V_PANEL, 1024);
-            auto issue_s = [&](uint32_t g, bool last) -> bool {   // S = Q K^T of tile g
-                const uint32_t stage = g % C::KS;
-                if (!warp_wait(C::BAR_K_FULL + stage, g / C::KS & 1, CHUNK_ERR_MMA))
-                    return false;
-                tc_fence_after();
-                if (leader) {
-                    const uint64_t dk = desc_k + (stage * C::STAGE >> 4);
+            // (the whole loop in one lane: groups of products issued from a branch that the
+            // warp's other lanes skip took twice the time of the products)
+            if (elect_one()) {
+                const uint64_t desc_q = D == 64 ? sdesc_sw64(base + C::OFF_Q, 16, 512) : sdesc_sw128(base + C::OFF_Q, 16, 1024);
+                const uint64_t desc_k = D == 64 ? sdesc_sw64(base + C::OFF_K, 16, 512) : sdesc_sw128(base + C::OFF_K, 16, 1024);
+                const uint64_t desc_v = sdesc_sw128(base + C::OFF_V, C::V_PANEL, 1024);
+                bool ok = true;
+                auto wait = [&](int i, uint32_t parity) {
+                    if (ok)
+                        ok = lone_wait(bar(i), parity, a.err, CHUNK_ERR_MMA | i, limit);
+                };
+                // S = Q K^T of row tile q and tile g of keys; of them all the last to read the tile
+                auto issue_s = [&](int q, uint32_t g, bool last_q, bool last_g) {
+                    const uint32_t stage = g % C::KS;
+                    const uint64_t dk = desc_k + (stage * C::STAGE >> 4), dq = desc_q + (q * C::Q_TILE >> 4);
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk) {
                             const int panel = kk * 32 / C::ROW, col = kk * 32 % C::ROW;
-                            mma_ss<true>(tmem + C::TM_S + g % C::SB * TILE,
-                                         desc_q + ((term * C::Q_TERM + panel * C::Q_PANEL + col) >> 4),
-                                         dk + ((panel * C::PANEL + col) >> 4), idesc_e4m3_f32(R, TILE, false, false),
+                            mma_ss<true>(tmem + C::TM_S + q * TILE, dq + ((term * C::Q_TERM + panel * C::Q_PANEL + col) >> 4),
+                                         dk + ((panel * C::PANEL + col) >> 4), idesc_e4m3_f32(128, TILE, false, false),
                                          term > 0 || kk > 0);
                         }
-                    mma_commit(bar(C::BAR_S_FULL + g % C::SB));
-                    mma_commit(bar(C::BAR_K_EMPTY + stage));
-                    if (last)
-                        mma_commit(bar(C::BAR_Q_EMPTY));
-                }
-                __syncwarp();
-                return true;
-            };
-            auto issue_pv = [&](uint32_t g, bool start) -> bool {   // O += P V of tile g
-                // a unit's first product overwrites O: the one before has been read out
-                if (!warp_wait(C::BAR_P_FULL + g % C::SB, g / C::SB & 1, CHUNK_ERR_MMA) ||
-                    (start && unit > 0 && !warp_wait(C::BAR_O_FREE, (unit - 1) & 1, CHUNK_ERR_MMA)))
-                    return false;
-                for (int half = 0; half < 2; ++half) {
-                    if (!warp_wait(C::BAR_V_FULL + half, g & 1, CHUNK_ERR_MMA))
-                        return false;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t dv = desc_v + (half * C::V_BYTES >> 4);
-                        const uint32_t p = tmem + C::TM_S + g % C::SB * TILE + half * (C::HALF / 2);
+                    mma_commit(bar(C::BAR_S_FULL + q));
+                    if (last_q)
+                        mma_commit(bar(C::BAR_K_EMPTY + stage));
+                    if (last_g)
+                        mma_commit(bar(C::BAR_Q_EMPTY + q));
+                };
+                auto issue_pv = [&](int q, uint32_t g, bool start, bool last_q) {   // O += P V
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t buf = (2 * g + half) % C::VB;
+                        const uint64_t dv = desc_v + (buf * C::V_BYTES >> 4);
+                        const uint32_t p = tmem + C::TM_S + q * TILE + half * (C::HALF / 2);
 #pragma unroll
                         for (int kk = 0; kk < C::HALF / 16; ++kk)
-                            mma_ts(tmem + C::TM_O, p + kk * 8, dv + (kk * 16 * 128 >> 4), C::idesc(D, true),
+                            mma_ts(tmem + C::TM_O + q * D, p + kk * 8, dv + (kk * 16 * 128 >> 4), C::idesc(D, true),
                                    !start || half > 0 || kk > 0);
-                        mma_commit(bar(C::BAR_V_EMPTY + half));
-                        if (half)
-                            mma_commit(bar(C::BAR_O_DONE));
+                        if (last_q)
+                            mma_commit(bar(C::BAR_V_EMPTY + buf));
                     }
-                    __syncwarp();
-                }
-                return true;
-            };
-            bool ok = true;
-            do {
-                int tile0, tile1;
-                part_of(tile0, tile1);
-                const int n = tile1 - tile0;
-                ok = warp_wait(C::BAR_Q_FULL, unit & 1, CHUNK_ERR_MMA);
-                for (int j = 0; j < C::SB && j < n && ok; ++j)
-                    ok = issue_s(it + j, j == n - 1);
-                for (int j = 0; j < n && ok; ++j) {
-                    ok = issue_pv(it + j, j == 0);
-                    if (ok && j + C::SB < n)
-                        ok = issue_s(it + j + C::SB, j + C::SB == n - 1);
-                }
-                it += n;
-                ++unit;
-            } while (ok && next_unit());
-            // nothing issued is still running when tensor memory is given back
-            if (leader)
+                    mma_commit(bar(C::BAR_O_DONE + q));
+                };
+                auto wait_k = [&](uint32_t g) { wait(C::BAR_K_FULL + g % C::KS, g / C::KS & 1); };
+                auto wait_v = [&](uint32_t item) { wait(C::BAR_V_FULL + item % C::VB, item / C::VB & 1); };
+                // of each row tile: tiles of keys, and units, before the present unit
+                uint32_t done[C::NQ] = {}, units[C::NQ] = {};
+                bool more;
+                do {
+                    int tile0, tile1;
+                    part_of(tile0, tile1);
+                    const int n = tile1 - tile0, nq = row_tiles();
+                    wait_k(it);
+#pragma unroll
+                    for (int q = 0; q < C::NQ; ++q)
+                        if (q < nq) {
+                            wait(C::BAR_Q_FULL + q, units[q] & 1);
+                            if (ok) {
+                                tc_fence_after();
+                                issue_s(q, it, q == nq - 1, n == 1);
+                            }
+                        }
+                    for (int j = 0; j < n && ok; ++j) {
+                        // (keys and values first: when the weights are there, this tile's and
+                        // the next one's products go out in one run)
+                        wait_v(2 * (it + j));
+                        wait_v(2 * (it + j) + 1);
+                        if (j + 1 < n)
+                            wait_k(it + j + 1);
+#pragma unroll
+                        for (int q = 0; q < C::NQ; ++q)
+                            if (q < nq) {
+                                // a unit's first product overwrites O: the one before has been read out
+                                if (j == 0 && units[q] > 0)
+                                    wait(C::BAR_O_FREE + q, (units[q] - 1) & 1);
+                                wait(C::BAR_P_FULL + q, (done[q] + j) & 1);
+                                if (ok) {
+                                    tc_fence_after();
+                                    issue_pv(q, it + j, j == 0, q == nq - 1);
+                                    if (j + 1 < n)
+                                        issue_s(q, it + j + 1, q == nq - 1, j + 2 == n);
+                                }
+                            }
+                    }
+                    it += n;
+#pragma unroll
+                    for (int q = 0; q < C::NQ; ++q)
+                        if (q < nq) {
+                            done[q] += n;
+                            ++units[q];
+                        }
+                    Line<C> &mine = sh.line[C::WARP_MMA];
+                    more = ok && mine.next(a) && mine.at < sh.end;
+                } while (more);
+                // nothing issued is still running when tensor memory is given back
                 mma_commit(bar(C::BAR_DRAIN));
+                lone_wait(bar(C::BAR_DRAIN), 0, a.err, CHUNK_ERR_DRAIN | C::BAR_DRAIN, limit);
+            }
             __syncwarp();
-            warp_wait(C::BAR_DRAIN, 0, CHUNK_ERR_DRAIN);
         } else if (warp == C::WARP_LOAD) {
             // ======================================== pages -> stages
             const int box_shift = a.c.page_shift;              // rows of a box: a page
@@ -413,7 +440,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         // times a weight of 0 is NaN: such values become zeros here, and their
                         // places go to the softmax warps.  Keys that no row sees are zeros, too
                         // (without a page, what lies in their place may be anything).
-                        uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + (g & 1) * C::NAN_BYTES);
+                        uint16_t *const map = reinterpret_cast<uint16_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
 #pragma unroll
                         for (int i = 0; i < NL; ++i) {
                             const int row = half * C::HALF + row0 + 32 * (i & 1), pos = from + j * TILE + row;
@@ -434,14 +461,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     }
                     if (half)
                         warp_arrive(C::BAR_RAW_EMPTY + stage);
-                    if (g >= 1 && !(ok = warp_wait(C::BAR_V_EMPTY + half, (g - 1) & 1, CHUNK_ERR_CONVERT)))
+                    const uint32_t item = 2 * g + half, buf = item % C::VB;
+                    if (item >= C::VB && !(ok = warp_wait(C::BAR_V_EMPTY + buf, (item / C::VB - 1) & 1, CHUNK_ERR_CONVERT)))
                         break;
 #pragma unroll
                     for (int i = 0; i < NL; ++i)
-                        store_f16(base + C::OFF_V + half * C::V_BYTES + (i >> 1) * C::V_PANEL + (row0 + 32 * (i & 1)) * 128, row0,
+                        store_f16(base + C::OFF_V + buf * C::V_BYTES + (i >> 1) * C::V_PANEL + (row0 + 32 * (i & 1)) * 128, row0,
                                   c * 2, v[i]);
                     fence_proxy_async_shared();
-                    warp_arrive(C::BAR_V_FULL + half);
+                    warp_arrive(C::BAR_V_FULL + buf);
                 }
             }
             it += n;
@@ -450,22 +478,25 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         // ============================================ softmax: two threads a row
         if constexpr (C::REG_SPLIT)
             setmaxnreg_inc<C::REG_SOFTMAX>();
-        const int half = warp >> 2, row = tid & (R - 1);       // keys 64 half .. of a tile, columns D / 2 half .. of O
+        // row tile, row in it; keys 64 half .. of a tile, columns D / 2 half .. of O
+        const int rt = warp >> 3, row = tid & 127, half = warp >> 2 & 1;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float scale_log2 = a.scale * 1.4426950408889634f;
-        const uint32_t o_addr = tmem + lanes + C::TM_O;
+        const uint32_t o_addr = tmem + lanes + C::TM_O + rt * D, s_addr = tmem + lanes + C::TM_S + rt * TILE;
+        auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + rt) : "memory"); };   // the row tile's warps
         // the two warps of the same rows
-        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
+        const int pair_id = 3 + rt * 4 + (warp & 3);
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory"); };
         auto pair_any = [&](bool x) -> bool {
             uint32_t r;
             asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
                          "bar.red.or.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                          : "=r"(r)
-                         : "r"(1 + (warp & 3)), "r"(static_cast<uint32_t>(x))
+                         : "r"(pair_id), "r"(static_cast<uint32_t>(x))
                          : "memory");
             return r != 0;
         };
-        float *const pair = reinterpret_cast<float *>(smem + C::OFF_PAIR);   // [2][R]
+        float *const pair = reinterpret_cast<float *>(smem + C::OFF_PAIR);   // by thread
         // A wait that ran out is recorded and not waited for again: the role runs on to its end
         // without waiting (its outputs are undefined), so that barriers between warps still match.
         bool ok = true;
@@ -473,13 +504,17 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             if (ok)
                 ok = warp_wait(i, parity, CHUNK_ERR_SOFTMAX);
         };
-        uint32_t group_phase = 0;
+        uint32_t n_done = 0, unit = 0;                         // of this row tile
         do {
             int tile0, tile1;
             part_of(tile0, tile1);
             const int n = tile1 - tile0;
+            if (rt >= row_tiles()) {
+                it += n;
+                continue;
+            }
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
-            const int rr = line.rb * R + row;
+            const int rr = line.rb * R + rt * 128 + row;
             const bool live = rr < line.s.n * a.G;
             const int tok = rr / a.G, hq = line.h * a.G + rr % a.G;
             int lo = 0, hi = 0;                                  // keys the row sees
@@ -510,7 +545,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // a row with an infinity or NaN has no finite scores: make it NaN
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
                 if (unit > 0)
-                    wait(C::BAR_Q_EMPTY, (unit - 1) & 1);
+                    wait(C::BAR_Q_EMPTY + rt, (unit - 1) & 1);
 #pragma unroll 2
                 for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
                     uint32_t t0[4], t1[4];
@@ -527,44 +562,64 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         }
                     }
                     const int panel = c * 16 / C::ROW, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
-                    const uint32_t at = base + C::OFF_Q + panel * C::Q_PANEL + row * C::ROW + ((c % (C::ROW / 16) ^ x) << 4);
+                    const uint32_t at = base + C::OFF_Q + rt * C::Q_TILE + panel * C::Q_PANEL + row * C::ROW + ((c % (C::ROW / 16) ^ x) << 4);
                     st_shared_v4(at, t0[0], t0[1], t0[2], t0[3]);
                     st_shared_v4(at + C::Q_TERM, t1[0], t1[1], t1[2], t1[3]);
                 }
                 fence_proxy_async_shared();
-                warp_arrive(C::BAR_Q_FULL);
+                warp_arrive(C::BAR_Q_FULL + rt);
             }
 
             const float scale_row = scale_log2 * pow2i(e);
             float M = -INFINITY, l = 0.f;                        // (M: the same in both threads)
             // values of O that a visible NaN value makes NaN (the first thread's to set)
-            uint32_t *const mark = reinterpret_cast<uint32_t *>(smem + C::OFF_MARK) + row;   // word q: [q * R]
+            uint32_t *const mark = reinterpret_cast<uint32_t *>(smem + C::OFF_MARK) + rt * 128 + row;   // word w: [w * R]
             if (half == 0)
 #pragma unroll
-                for (int q = 0; q < C::NAN_WORDS; ++q)
-                    mark[q * R] = 0;
+                for (int w = 0; w < C::NAN_WORDS; ++w)
+                    mark[w * R] = 0;
             for (int j = 0; j < n; ++j) {
-                const uint32_t g = it + j, buf = g % C::SB;
-                wait(C::BAR_S_FULL + buf, g / C::SB & 1);
+                const uint32_t g = it + j, d = n_done + j;
+                wait(C::BAR_S_FULL + rt, d & 1);
                 tc_fence_after();
-                const uint32_t s_addr = tmem + lanes + C::TM_S + buf * TILE;
                 const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES);
                 const int pos0 = from + j * TILE;
                 const bool whole = is_whole(smem, g);
                 if (!whole) {            // NaN values, once the tile's are converted
-                    wait(C::BAR_V_FULL, g & 1);
-                    wait(C::BAR_V_FULL + 1, g & 1);
+                    for (uint32_t item = 2 * g; item < 2 * g + 2; ++item)
+                        wait(C::BAR_V_FULL + item % C::VB, item / C::VB & 1);
                     if (half == 0 && *reinterpret_cast<const uint32_t *>(smem + C::OFF_FLAGS + (g & 3) * 4)) {
-                        const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + (g & 1) * C::NAN_BYTES);
+                        const uint32_t *map = reinterpret_cast<const uint32_t *>(smem + C::OFF_NAN + (g & 3) * C::NAN_BYTES);
 #pragma unroll 1
                         for (int k = 0; k < TILE; ++k)
                             if (pos0 + k >= lo && pos0 + k < hi)
 #pragma unroll
-                                for (int q = 0; q < C::NAN_WORDS; ++q)
-                                    mark[q * R] |= map[k * C::NAN_WORDS + q];
+                                for (int w = 0; w < C::NAN_WORDS; ++w)
+                                    mark[w * R] |= map[k * C::NAN_WORDS + w];
                     }
                 }
-                // this thread's scores, 16 at a time; those that the row does not see are -inf
+                // Scores that the row does not see become -inf where they are: the passes over them
+                // below, the same for every tile, then have no branch to keep their parts apart.
+                if (!whole) {
+#pragma unroll 1
+                    for (int i = 0; i < GROUPS / 2; ++i) {
+                        uint32_t r[CHUNK];
+                        tmem_ld(s_addr + half * C::HALF + i * CHUNK, r);
+                        tmem_wait_ld();
+                        tmem_pin(r);
+                        const uint32_t word = __float_as_uint(info[half * (GROUPS / 2) + i].w);
+                        const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
+                        const int key0 = pos0 + half * C::HALF + i * CHUNK;
+#pragma unroll
+                        for (int k = 0; k < CHUNK; ++k) {
+                            const bool see = page && key0 + k >= lo && key0 + k < hi;
+                            r[k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[k];
+                        }
+                        tmem_st16(s_addr + half * C::HALF + i * CHUNK, r);
+                    }
+                    tmem_st_wait();
+                }
+                // this thread's scores, 16 at a time
                 auto for_groups = [&](auto f) {
                     uint32_t r[2][CHUNK];
                     tmem_ld(s_addr + half * C::HALF, r[0]);
@@ -575,16 +630,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         if (i + 1 < GROUPS / 2)
                             tmem_ld(s_addr + half * C::HALF + (i + 1) * CHUNK, r[(i + 1) & 1]);
                         const float4 scales = info[half * (GROUPS / 2) + i];
-                        if (!whole) {
-                            const uint32_t word = __float_as_uint(scales.w);
-                            const bool page = word & PAGE_BIT, nan_scale = (word & 255) == 255;
-                            const int key0 = pos0 + half * C::HALF + i * CHUNK;
-#pragma unroll
-                            for (int k = 0; k < CHUNK; ++k) {
-                                const bool see = page && key0 + k >= lo && key0 + k < hi;
-                                r[i & 1][k] = !see ? 0xff800000u : nan_scale ? 0x7fc00000u : r[i & 1][k];
-                            }
-                        }
                         // (not 0: a hidden score is -inf * c)
                         f(i, r[i & 1], fmaxf(scale_row * scales.x, 1.17549435e-38f), scales.y, scales.z);
                     }
@@ -609,7 +654,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         });
                         pair[tid] = top;
                         pair_sync();
-                        top = fmaxf(top, pair[tid ^ R]);
+                        top = fmaxf(top, pair[tid ^ 128]);
                         float f = 1.f;
                         if (top > M) {
                             f = ex2_approx(M - top);
@@ -618,7 +663,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         }
                         if (j > 0) {             // O in tensor memory stands for the old maximum
                             if (!waited)
-                                wait(C::BAR_O_DONE, (g - 1) & 1);
+                                wait(C::BAR_O_DONE + rt, (d - 1) & 1);
                             waited = true;
                             tc_fence_after();
 #pragma unroll 1
@@ -665,19 +710,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // tile's product (below) needs that for the last but one's, before the last can
                 // complete.
                 if (!waited && j == n - 1)
-                    wait(C::BAR_O_DONE, (g - 1) & 1);
+                    wait(C::BAR_O_DONE + rt, (d - 1) & 1);
+                // over the first half of S
                 tmem_st32(s_addr + half * 32, p);
                 tmem_st_wait();
                 tc_fence_before();
-                warp_arrive(C::BAR_P_FULL + buf);
+                warp_arrive(C::BAR_P_FULL + rt);
             }
 
             // ---- O out of tensor memory: the unit's rows, or this part of them
             it += n;
+            n_done += n;
             pair[tid] = l;
             pair_sync();
-            l = (half ? pair[row] : l) + (half ? l : pair[R + row]);   // (in one order)
-            wait(C::BAR_O_DONE, (it - 1) & 1);
+            l = (half ? pair[tid ^ 128] : l) + (half ? l : pair[tid ^ 128]);   // (in one order)
+            wait(C::BAR_O_DONE + rt, (n_done - 1) & 1);
             tc_fence_after();
             const int first_cta = cut ? sh.range.owner(line.at) : cta;
             const int last_cta = cut ? sh.range.owner(line.at + line.span.tiles - 1) : cta;
@@ -708,11 +755,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 } else if (!alone) {
 #pragma unroll
                     for (int k = 0; k < 16; k += 4)
-                        *reinterpret_cast<uint4 *>(part + row * D + cc * 16 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                        *reinterpret_cast<uint4 *>(part + (rt * 128 + row) * D + cc * 16 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
                 }
             }
             tc_fence_before();
-            warp_arrive(C::BAR_O_FREE);
+            warp_arrive(C::BAR_O_FREE + rt);
             auto write_lse = [&](int r, float v) {
                 const int x = line.rb * R + r;
                 if (x < line.s.n * a.G)
@@ -721,24 +768,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             };
             if (alone) {
                 if (half == 0)
-                    write_lse(row, lse2);
+                    write_lse(rt * 128 + row, lse2);
             } else {
                 if (half == 0)
-                    part[R * D + row] = lse2;
-                // the CTA whose part is the last to arrive merges them
-                auto group = [&] {
-                    warp_arrive(C::BAR_GROUP);
-                    wait(C::BAR_GROUP, group_phase++ & 1);
-                };
+                    part[R * D + rt * 128 + row] = lse2;
+                // the CTA whose part is the last to arrive merges them, each row tile by itself
                 __threadfence();
-                group();
-                volatile int *const last = reinterpret_cast<int *>(smem + C::OFF_MISC + 4);
-                if (tid == 0) {
-                    *last = atomicAdd(parts.counters + first_cta, 1) == last_cta - first_cta;
+                tile_sync();
+                volatile int *const last = reinterpret_cast<int *>(smem + C::OFF_MISC + 4) + rt;
+                if ((tid & 255) == 0) {
+                    int *const counter = parts.counters + 2 * first_cta + rt;
+                    *last = atomicAdd(counter, 1) == last_cta - first_cta;
                     if (*last)
-                        parts.counters[first_cta] = 0;
+                        *counter = 0;
                 }
-                group();
+                tile_sync();
                 if (*last) {
                     __threadfence();
                     auto write_o = [&](int r, int u, const float4 &v) {
@@ -747,8 +791,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                                        static_cast<long long>(x / a.G) * a.o_sl;
                         *reinterpret_cast<uint2 *>(to + u * 4) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     };
-                    const int live_rows = line.s.n * a.G - line.rb * R;
-                    merge_parts<C>(parts, first_cta, last_cta, live_rows < R ? live_rows : R, tid, 2 * R, write_o, write_lse);
+                    const int live_rows = line.s.n * a.G - line.rb * R, end_row = (rt + 1) * 128;
+                    merge_parts<C>(parts, first_cta, last_cta, rt * 128, live_rows < end_row ? live_rows : end_row, tid & 255, 256,
+                                   write_o, write_lse);
                 }
             }
             ++unit;

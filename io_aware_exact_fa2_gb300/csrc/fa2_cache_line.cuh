@@ -10,8 +10,6 @@
 // Lengths are device data, so every CTA lays out the line for itself.
 #pragma once
 
-#include <climits>
-
 #include "fa2_cache.cuh"
 #include "sm103_ptx.cuh"
 
@@ -22,12 +20,15 @@ constexpr int CHUNK = 16;                 // keys of the smallest piece; divides
 // Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
 // R rows: O [R, D] fp32, then the log2-sum-exp2 [R].
 struct Parts {
-    int *counters;      // [grid]
+    int *counters;      // [grid][2]: of the units that begin in a range and go on, arrived parts
     float *data;
     __host__ __device__ static constexpr size_t slot_floats(int R, int D) { return static_cast<size_t>(R) * (D + 1); }
-    __host__ __device__ static constexpr size_t counter_bytes(int grid)
+    // (the same for every configuration: calls of different ones may take the same workspace
+    // in turn, and none's data may lie where another's counters do)
+    static constexpr int MAX_CTAS = 4;   // an SM
+    __host__ __device__ static constexpr size_t counter_bytes(int num_sms)
     {
-        return (static_cast<size_t>(grid) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+        return (static_cast<size_t>(num_sms) * MAX_CTAS * 2 * sizeof(int) + 255) & ~static_cast<size_t>(255);
     }
 };
 
@@ -35,7 +36,8 @@ struct Parts {
 template <class C>
 size_t attn_workspace(int num_sms)
 {
-    return Parts::counter_bytes(num_sms * C::CTAS) +
+    static_assert(C::CTAS <= Parts::MAX_CTAS, "a counter pair a CTA");
+    return Parts::counter_bytes(num_sms) +
            static_cast<size_t>(num_sms) * C::CTAS * 2 * Parts::slot_floats(C::R, C::D) * sizeof(float);
 }
 
@@ -49,12 +51,15 @@ bool parts_of(const AttnArgs &a, Parts &parts)
     if (a.workspace_bytes < attn_workspace<C>(a.num_sms))
         return false;
     parts.counters = static_cast<int *>(a.workspace);
-    parts.data = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + Parts::counter_bytes(a.num_sms * C::CTAS));
+    parts.data = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + Parts::counter_bytes(a.num_sms));
     return true;
 }
 
+// Places on the line: an int counts them, with room for what is added to a place.
+constexpr int MAX_LINE = 1 << 30;
+
 // CTAs to launch: no more than the longest sequences could make ranges for; 0 if the line
-// could be longer than an int can count.
+// could be longer than that.
 template <class C>
 int line_grid(const AttnArgs &a, bool cut)
 {
@@ -62,7 +67,7 @@ int line_grid(const AttnArgs &a, bool cut)
     const long long blocks = (static_cast<long long>(a.Lq) * a.G + C::R - 1) / C::R;
     const long long length = ((static_cast<long long>(a.c.max_pages) << a.c.page_shift) + C::TILE - 1) / C::TILE + 1 + C::UNIT_COST;
     const long long units = static_cast<long long>(a.c.B) * a.c.H * blocks;   // (B H, blocks < 2^31)
-    if (units > INT_MAX || units * length > INT_MAX)
+    if (units > MAX_LINE || units * length > MAX_LINE)
         return 0;
     const long long grid = cut ? (units * length + C::MIN_TILES - 1) / C::MIN_TILES : units;
     return static_cast<int>(grid > most ? most : grid);
@@ -264,15 +269,15 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
 
 // Merges the parts of a unit that ranges c0 .. c1 computed, always in that order, by
 // `threads` threads of which the caller is number `tid`; write(row, unit, value) takes
-// four values of O, write_lse(row, value) the log2-sum-exp2 of the first `rows` rows.
+// four values of O, write_lse(row, value) the log2-sum-exp2, of rows row0 .. row1 - 1.
 template <class C, class W, class L>
-__device__ __forceinline__ void merge_parts(const Parts &parts, int c0, int c1, int rows, int tid, int threads, W write,
+__device__ __forceinline__ void merge_parts(const Parts &parts, int c0, int c1, int row0, int row1, int tid, int threads, W write,
                                             L write_lse)
 {
     constexpr int R = C::R, D = C::D;
     const size_t slot_floats = Parts::slot_floats(R, D);
     auto slot = [&](int c) { return parts.data + (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * slot_floats; };
-    for (int i = tid; i < rows * (D / 4); i += threads) {
+    for (int i = row0 * (D / 4) + tid; i < row1 * (D / 4); i += threads) {
         const int r = i / (D / 4), u = i % (D / 4);
         float top = -INFINITY;
         for (int c = c0; c <= c1; ++c)

@@ -632,9 +632,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 __threadfence();
                 sync();
                 if (tid == 0) {
-                    *last = atomicAdd(parts.counters + first_cta, 1) == last_cta - first_cta;
+                    int *const counter = parts.counters + 2 * first_cta;
+                    *last = atomicAdd(counter, 1) == last_cta - first_cta;
                     if (*last)
-                        parts.counters[first_cta] = 0;
+                        *counter = 0;
                 }
                 sync();
                 if (*last) {
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             *reinterpret_cast<uint2 *>(o + sh_place[r].x + u * 4) =
                                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     };
-                    merge_parts<C>(parts, first_cta, last_cta, live < R ? live : R, tid, 128, write_o, write_lse);
+                    merge_parts<C>(parts, first_cta, last_cta, 0, live < R ? live : R, tid, 128, write_o, write_lse);
                 }
             }
             ++unit;
