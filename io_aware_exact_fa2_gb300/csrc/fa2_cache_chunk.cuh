@@ -52,7 +52,7 @@ struct ChunkCfg {
     // With six warpgroups the launch leaves 80 registers a thread, 480 for the warpgroups'
     // lanes together: the softmax rises, the others give.
     static constexpr bool REG_SPLIT = NQ == 2;
-    static constexpr int REG_SOFTMAX = 88, REG_CONVERT = 64, REG_ISSUE = 64;
+    static constexpr int REG_SOFTMAX = 88, REG_CONVERT = 56, REG_ISSUE = 72;
     static_assert(4 * REG_SOFTMAX + REG_CONVERT + REG_ISSUE <= 6 * 80, "the split draws on the launch's registers");
     static constexpr int GROUPS = TILE / CHUNK;      // 16-key groups of a tile, each in one page
 
@@ -529,16 +529,23 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             // largest magnitude to [224, 448); each thread stores half of it
             int e;
             {
-                const uint16_t *q = static_cast<const uint16_t *>(a.q) + line.b * a.q_sb + hq * a.q_sh + tok * a.q_sl;
+                const uint16_t *q =
+                    static_cast<const uint16_t *>(a.q) + line.b * a.q_sb + hq * a.q_sh + tok * a.q_sl + half * (D / 2);
+                uint4 x[D / 16];
                 uint32_t top = 0;
-#pragma unroll 8
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                    x[c] = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
                 }
+                pair[tid] = __uint_as_float(top);
+                pair_sync();
+                top = max(top, __float_as_uint(pair[tid ^ 128]));
                 // 448 = 1.75 * 2^8
                 e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) >= 0x60u ? 1 : 0);
                 e = e < -126 ? -126 : e;
@@ -546,13 +553,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
                 if (unit > 0)
                     wait(C::BAR_Q_EMPTY + rt, (unit - 1) & 1);
-#pragma unroll 2
-                for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
                     uint32_t t0[4], t1[4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(q) + c * 2 + i) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        const uint32_t w[4] = {x[c * 2 + i].x, x[c * 2 + i].y, x[c * 2 + i].z, x[c * 2 + i].w};
 #pragma unroll
                         for (int k = 0; k < 4; k += 2) {
                             uint32_t y0 = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
@@ -561,8 +567,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             t1[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
                         }
                     }
-                    const int panel = c * 16 / C::ROW, x = C::ROW == 64 ? row >> 1 & 3 : row & 7;
-                    const uint32_t at = base + C::OFF_Q + rt * C::Q_TILE + panel * C::Q_PANEL + row * C::ROW + ((c % (C::ROW / 16) ^ x) << 4);
+                    const int col = half * (D / 32) + c, panel = col * 16 / C::ROW, swizzle = C::ROW == 64 ? row >> 1 & 3 : row & 7;
+                    const uint32_t at = base + C::OFF_Q + rt * C::Q_TILE + panel * C::Q_PANEL + row * C::ROW +
+                                        ((col % (C::ROW / 16) ^ swizzle) << 4);
                     st_shared_v4(at, t0[0], t0[1], t0[2], t0[3]);
                     st_shared_v4(at + C::Q_TERM, t1[0], t1[1], t1[2], t1[3]);
                 }
@@ -734,6 +741,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             uint16_t *const o = static_cast<uint16_t *>(a.o) + line.b * a.o_sb + hq * a.o_sh + tok * a.o_sl;
             float *const part =
                 cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
+            // a part's quadruple u of columns: neighbouring threads' rows lie next to each other
+            auto place = [&](int u) { return (u * R + rt * 128 + row) * 4; };
 #pragma unroll 1
             for (int cc = half * (D / 32); cc < (half + 1) * (D / 32); ++cc) {   // 16 columns
                 uint32_t r[16];
@@ -755,20 +764,17 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 } else if (!alone) {
 #pragma unroll
                     for (int k = 0; k < 16; k += 4)
-                        *reinterpret_cast<uint4 *>(part + (rt * 128 + row) * D + cc * 16 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                        *reinterpret_cast<uint4 *>(part + place(cc * 4 + k / 4)) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
                 }
             }
             tc_fence_before();
             warp_arrive(C::BAR_O_FREE + rt);
-            auto write_lse = [&](int r, float v) {
-                const int x = line.rb * R + r;
-                if (x < line.s.n * a.G)
-                    a.lse[(static_cast<long long>(line.b) * a.Hq + line.h * a.G + x % a.G) * a.Lq + x / a.G] =
-                        v * 0.69314718055994531f;
+            auto write_lse = [&](float v) {
+                a.lse[(static_cast<long long>(line.b) * a.Hq + hq) * a.Lq + tok] = v * 0.69314718055994531f;
             };
             if (alone) {
-                if (half == 0)
-                    write_lse(rt * 128 + row, lse2);
+                if (half == 0 && live)
+                    write_lse(lse2);
             } else {
                 if (half == 0)
                     part[R * D + rt * 128 + row] = lse2;
@@ -785,15 +791,21 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 tile_sync();
                 if (*last) {
                     __threadfence();
-                    auto write_o = [&](int r, int u, const float4 &v) {
-                        const int x = line.rb * R + r;
-                        uint16_t *to = static_cast<uint16_t *>(a.o) + line.b * a.o_sb + (line.h * a.G + x % a.G) * a.o_sh +
-                                       static_cast<long long>(x / a.G) * a.o_sl;
-                        *reinterpret_cast<uint2 *>(to + u * 4) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                    };
-                    const int live_rows = line.s.n * a.G - line.rb * R, end_row = (rt + 1) * 128;
-                    merge_parts<C>(parts, first_cta, last_cta, rt * 128, live_rows < end_row ? live_rows : end_row, tid & 255, 256,
-                                   write_o, write_lse);
+#pragma unroll 1
+                    for (int cc = half; cc < D / 16; cc += 2) {
+                        float4 v[4];
+                        const float merged =
+                            merge_row<C, 4>(parts, first_cta, last_cta, rt * 128 + row, [&](int k) { return place(cc * 4 + k); }, v);
+                        if (live) {
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2)
+                                *reinterpret_cast<uint4 *>(o + cc * 16 + k * 4) =
+                                    make_uint4(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w),
+                                               pack_bf16x2(v[k + 1].x, v[k + 1].y), pack_bf16x2(v[k + 1].z, v[k + 1].w));
+                            if (cc == 0)
+                                write_lse(merged);
+                        }
+                    }
                 }
             }
             ++unit;

@@ -18,7 +18,7 @@ namespace cache {
 
 constexpr int CHUNK = 16;                 // keys of the smallest piece; divides every page size
 // Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
-// R rows: O [R, D] fp32, then the log2-sum-exp2 [R].
+// R rows: O fp32, R D of them in the kernel's own order, then the log2-sum-exp2 [R].
 struct Parts {
     int *counters;      // [grid][2]: of the units that begin in a range and go on, arrived parts
     float *data;
@@ -267,36 +267,49 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     return line.at < end;
 }
 
-// Merges the parts of a unit that ranges c0 .. c1 computed, always in that order, by
-// `threads` threads of which the caller is number `tid`; write(row, unit, value) takes
-// four values of O, write_lse(row, value) the log2-sum-exp2, of rows row0 .. row1 - 1.
-template <class C, class W, class L>
-__device__ __forceinline__ void merge_parts(const Parts &parts, int c0, int c1, int row0, int row1, int tid, int threads, W write,
-                                            L write_lse)
+// Merges what ranges c0 .. c1 computed of N quadruples of one row of a unit, always in that
+// order: place(k) is quadruple k's offset in a slot.  Returns the row's log2-sum-exp2.  (One
+// pass, two parts at a time: the loads of a thread's quadruples are under way together, where
+// a pass for the maximum and one a quadruple waited for one load after the other.  Ragged
+// prompts merged in 13 us that way.)
+template <class C, int N, class P>
+__device__ __forceinline__ float merge_row(const Parts &parts, int c0, int c1, int row, P place, float4 (&v)[N])
 {
-    constexpr int R = C::R, D = C::D;
-    const size_t slot_floats = Parts::slot_floats(R, D);
+    const size_t slot_floats = Parts::slot_floats(C::R, C::D);
     auto slot = [&](int c) { return parts.data + (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * slot_floats; };
-    for (int i = row0 * (D / 4) + tid; i < row1 * (D / 4); i += threads) {
-        const int r = i / (D / 4), u = i % (D / 4);
-        float top = -INFINITY;
-        for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(slot(c) + R * D + r));
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float f = ptx::ex2_approx(__ldcg(slot(c) + R * D + r) - ref);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot(c)) + i);
-            l += f;
-            v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+    float top = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c = c0; c <= c1; c += 2) {
+        const bool two = c < c1;
+        const float *const s0 = slot(c), *const s1 = slot(c + 1);
+        const float a0 = __ldcg(s0 + C::R * C::D + row), a1 = two ? __ldcg(s1 + C::R * C::D + row) : -INFINITY;
+        float4 x0[N], x1[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            x0[k] = __ldcg(reinterpret_cast<const float4 *>(s0 + place(k)));
+            x1[k] = two ? __ldcg(reinterpret_cast<const float4 *>(s1 + place(k))) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-        write(r, u, v);
-        if (u == 0)
-            write_lse(r, l == 0.f ? -INFINITY : ref + ptx::lg2_approx(l));
+        const float before = top;
+        top = fmaxf(top, fmaxf(a0, a1));
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = ptx::ex2_approx(before - ref), f0 = ptx::ex2_approx(a0 - ref), f1 = ptx::ex2_approx(a1 - ref);
+        l = l * f + f0 + f1;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            v[k].x = v[k].x * f + x0[k].x * f0 + x1[k].x * f1;
+            v[k].y = v[k].y * f + x0[k].y * f0 + x1[k].y * f1;
+            v[k].z = v[k].z * f + x0[k].z * f0 + x1[k].z * f1;
+            v[k].w = v[k].w * f + x0[k].w * f0 + x1[k].w * f1;
+        }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        v[k].x *= inv, v[k].y *= inv, v[k].z *= inv, v[k].w *= inv;
+    return l == 0.f ? -INFINITY : top + ptx::lg2_approx(l);
 }
 #endif
 

@@ -640,12 +640,19 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 sync();
                 if (*last) {
                     __threadfence();
-                    auto write_o = [&](int r, int u, const float4 &v) {
-                        if (r < live)
-                            *reinterpret_cast<uint2 *>(o + sh_place[r].x + u * 4) =
-                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                    };
-                    merge_parts<C>(parts, first_cta, last_cta, 0, live < R ? live : R, tid, 128, write_o, write_lse);
+                    // N quadruples a thread, so that one pass takes the block (two at R D = 4096)
+                    constexpr int N = R * D >= 2048 ? 4 : R * D / 512, TPR = D / 4 / N;
+                    for (int r = tid / TPR; r < (live < R ? live : R); r += 128 / TPR) {
+                        float4 v[N];
+                        auto column = [&](int k) { return (tid % TPR + k * TPR) * 4; };
+                        const float lse2 = merge_row<C, N>(parts, first_cta, last_cta, r, [&](int k) { return r * D + column(k); }, v);
+#pragma unroll
+                        for (int k = 0; k < N; ++k)
+                            *reinterpret_cast<uint2 *>(o + sh_place[r].x + column(k)) =
+                                make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
+                        if (tid % TPR == 0)
+                            write_lse(r, lse2);
+                    }
                 }
             }
             ++unit;
