@@ -6,16 +6,12 @@ namespace fa2 {
 namespace cache {
 
 namespace {
-// Query rows of a key/value head (Lq G): blocks of 8 or 16 stream the cache with the rows
-// as columns of the products; more are rows themselves, 128 at a time.
-constexpr long long kFewRows = 64;
-
 template <class F>
 auto dispatch(long long rows, F f)
 {
-    if (rows <= 8)
+    if (rows <= kStepRows / 2)
         return f(StepCfg<256, 8>{});
-    if (rows <= kFewRows)
+    if (rows <= kStepRows)
         return f(StepCfg<256, 16>{});
     return f(ChunkCfg<256>{});
 }

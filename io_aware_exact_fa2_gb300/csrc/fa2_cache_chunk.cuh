@@ -44,7 +44,7 @@ struct ChunkCfg {
     static constexpr int NQ = D == 256 ? 1 : 2;      // 128-row tiles of a unit
     static constexpr int R = 128 * NQ;               // its query rows
     static constexpr int TILE = 128;                 // keys
-    static constexpr int UNIT_COST = 3, MIN_TILES = 2;   // see fa2_cache_line.cuh
+    static constexpr int UNIT_COST = 4, MIN_TILES = 3;   // see fa2_cache_line.cuh
     static constexpr int ALIGN = TILE;               // a tile begins at a multiple
     static constexpr int CTAS = 1;                   // an SM
     static constexpr int WARP_CONVERT = 8 * NQ, WARP_MMA = WARP_CONVERT + 4, WARP_LOAD = WARP_MMA + 1;

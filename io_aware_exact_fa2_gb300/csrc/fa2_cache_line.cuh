@@ -17,6 +17,10 @@ namespace fa2 {
 namespace cache {
 
 constexpr int CHUNK = 16;                 // keys of the smallest piece; divides every page size
+// Query rows of a key/value head (Lq G) up to which they are columns of the products, in a
+// block of 8 or 16 (fa2_cache_step.cuh); more are rows, 256 a block (fa2_cache_chunk.cuh).
+constexpr long long kStepRows = 16;
+
 // Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
 // R rows: O fp32, R D of them in the kernel's own order, then the log2-sum-exp2 [R].
 struct Parts {

@@ -84,7 +84,7 @@ def attention(q, kc, vc, ks, vs, table, kv_lens, q_lens, causal, window, scale):
     The bounds, per row, from the kernels' arithmetic.  q is two e4m3 terms, whose products
     with codes are exact; a bf16 has no more bits than they, but an element far below its
     row's largest is off by up to half the smallest step of the last term: with that largest
-    at least 128 (up to 64 rows a key/value head), and the last term's step 2^-9 / 16, 2^-21
+    at least 128 (up to 16 rows a key/value head), and the last term's step 2^-9 / 16, 2^-21
     of it; with the largest at least 224 and a step of 2^-9 (more rows), 2^-17.  A score sums
     2 D products in fp32, each addition off by at most 2^-23 of the partial sum (a bound for
     truncating adders too).  So a score is off by at most ds =
@@ -128,7 +128,7 @@ def attention(q, kc, vc, ks, vs, table, kv_lens, q_lens, causal, window, scale):
                         lse[b, h, i] = top + math.log(z)
                         o[b, h, i] = w @ vv
                         reach = scale * (np.abs(kk) @ np.abs(row)).max()
-                        small_q = scale * (2.0 ** -21 if Lq * Hq // H <= 64 else 2.0 ** -17) * np.abs(row).max() * np.abs(kk).sum(1).max()
+                        small_q = scale * (2.0 ** -21 if Lq * Hq // H <= 16 else 2.0 ** -17) * np.abs(row).max() * np.abs(kk).sum(1).max()
                         ds = reach * 2 * D * 2.0 ** -23 + small_q + 2.0 ** -21 * (1 + np.abs(s).max())
                         lb[b, h, i] = ds + len(s) * 2.0 ** -23 + 2.0 ** -21 * (1 + abs(lse[b, h, i]))
                         rel = 2.0 ** -11 + 2 * ds + len(s) * 2.0 ** -22
