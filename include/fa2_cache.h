@@ -120,9 +120,13 @@ fa2_status fa2_cache_read(const fa2_cache *c, void *k, void *v, const long long 
  *
  * Visible: 0 <= j < kv_lens[b], with a page; with causal != 0 also j <= pos(i);
  * with window >= 0 (causal only) also j >= pos(i) - window.  A row that sees
- * nothing gets O = 0 and LSE = -infinity.  The products are exact, sums and
- * softmax are fp32, softmax weights are rounded to fp16 (11 bits) for the
- * product with V.
+ * nothing gets O = 0 and LSE = -infinity.  The products run on the cache's codes
+ * as they are, with q as a sum of two e4m3 numbers times a power of two of its row:
+ * that is q itself but for elements far below their row's largest, which are off by
+ * at most 2^-21 of it (up to 16 rows, Lq * Hq / H) or 2^-17 (more).  Sums and softmax
+ * are fp32; softmax weights are rounded to three e4m3 terms (12 bits; up to 16 rows)
+ * or to fp16 (11 bits) for the product with V.  A row of q with an infinity or NaN
+ * gives NaN.
  *
  *   q          bf16 [B, Hq, Lq, D] device view, strides (batch, head, row) or NULL.
  *   o          bf16 [B, Hq, Lq, D] device view (written), likewise; rows must not overlap.
@@ -140,9 +144,9 @@ fa2_status fa2_cache_read(const fa2_cache *c, void *k, void *v, const long long 
  *              work.  Calls that may run at the same time must not share one.
  *
  * Results do not depend on timing: the parts of a row are merged in a fixed order.
- * The work of a call is counted in tiles of 128 keys by blocks of 8 to 128 of a
- * key/value head's Lq * Hq / H rows; sizes for which max_pages full pages would
- * make 2^31 of them or more are refused (FA2_ERR_UNSUPPORTED).
+ * The work of a call is counted in tiles of 128 keys by blocks of 8, 16, 128 or 256 of
+ * a key/value head's Lq * Hq / H rows; sizes for which max_pages full pages would make
+ * more than 2^30 of them are refused (FA2_ERR_UNSUPPORTED).
  * Errors as fa2_cache_write, also FA2_ERR_INVALID_ARG for a bad scale or window, Hq
  * not a multiple of H, or a workspace that is misaligned or too small.
  */
@@ -165,9 +169,10 @@ fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq, int D, in
  * kernel winds down.  Outputs of that call are then undefined, and a workspace it used
  * must be zero-filled again.
  *
- *   detail   optional: the raw code (0 = none), the waiting role in bits 8-11 (8
- *            softmax, 9 conversion, 10 MMA issuer, 11 a CTA's final wait for its
- *            own work), the barrier in the low byte.
+ *   detail   optional: the raw code (0 = none), the waiting role in bits 8-11, the
+ *            barrier in the low byte.  Roles, up to 16 rows: 12 softmax, 13 loading,
+ *            14 MMA issuer, 15 a CTA's final wait for its own work; more rows: 8, 11,
+ *            10 and 7, and 9 conversion.
  *
  * Returns FA2_OK, FA2_ERR_TIMEOUT, or FA2_ERR_CUDA.
  */

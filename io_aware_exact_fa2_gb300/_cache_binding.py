@@ -52,6 +52,7 @@ def load_cache_library() -> ctypes.CDLL:
 _lib = load_cache_library()
 _CODES, _BF16, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.int32
 _SCALES = (torch.float8_e8m0fnu, torch.uint8)
+_MAX_ROWS = 1 << 30   # of a sequence (the library's limit; checked here, too, for it takes an int)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -116,6 +117,8 @@ def _move(call, where, k_cache, v_cache, k_scale, v_scale, page_table, k, v, sta
     if k.ndim != 4:
         raise ValueError("k and v must be 4-D (B, H, L, D) views")
     L = k.shape[2]
+    if L > _MAX_ROWS:
+        raise ValueError("k and v must have at most 2^30 rows a sequence")
     shape = (B, H, L, D)
     ks, vs = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
     starts = _lengths("starts", starts, B, dev)
@@ -161,6 +164,8 @@ def fa2_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, o
     if q.ndim != 4:
         raise ValueError("q and o must be 4-D (B, Hq, Lq, D) views")
     Hq, Lq = q.shape[1:3]
+    if Lq > _MAX_ROWS:
+        raise ValueError("q and o must have at most 2^30 rows a sequence")
     shape = (B, Hq, Lq, D)
     qs, os_ = _rows("q", q, shape, dev), _rows("o", o, shape, dev)
     if lse.dtype is not torch.float32 or lse.shape != (B, Hq, Lq) or lse.get_device() != dev or not lse.is_contiguous():
@@ -175,8 +180,9 @@ def fa2_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, o
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
     if Lq == 0:   # (an empty tensor has no address)
         return
+    # (a window past the longest sequence hides nothing; -2 is refused)
     st = _lib.fa2_cache_attn(c, q.data_ptr(), o.data_ptr(), lse.data_ptr(), qs, os_, kv_lens, q_lens, Hq, Lq, bool(causal),
-                             -1 if window is None else window, D ** -0.5 if scale is None else scale, ws_ptr, ws_bytes,
+                             -1 if window is None else max(-2, min(int(window), _MAX_ROWS)), D ** -0.5 if scale is None else scale, ws_ptr, ws_bytes,
                              _stream(stream, dev))
     if st != 0:
         raise Fa2Error(st, "fa2_cache_attn")

@@ -476,7 +476,9 @@ def test_more_work_than_can_be_counted_is_refused():
     with pytest.raises(RuntimeError, match="FA2_ERR_UNSUPPORTED"):
         fa2().fa2_cache_attn(q, *dev, i32([40]), o, lse)
     # the same table with a row: every page is missing
-    fa2().fa2_cache_attn(q[:, :, :1].contiguous(), *dev, i32([1 << 30]), o[:, :, :1].contiguous(), lse[:, :, :1].contiguous())
+    q = q[:, :, :1].contiguous()
+    fa2().fa2_cache_attn(q, *dev, i32([1 << 30]), o[:, :, :1].contiguous(), lse[:, :, :1].contiguous(),
+                         workspace=fa2().fa2_cache_attn_workspace(q, dev[0]))
     assert fa2().fa2_cache_get_device_error() == (0, 0)
 
 
@@ -494,3 +496,120 @@ def test_a_small_workspace_is_refused():
         fa2().fa2_cache_attn(q, *dev, i32([40, 4]), o, lse)
     with pytest.raises(ValueError):
         fa2().fa2_cache_attn(q, *dev, torch.tensor([40]), o, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("window", [None, 0, 37, 130])
+def test_blocks_of_rows_over_pages_and_windows(D, page, window):
+    """17 rows and more: row tiles that end, begin and miss a block; strided pools and rows."""
+    lens = [290, 129, 77]
+    c = Cache(3, 2, D, page, lens, seed=D + page, slot_major=page != 64)
+    attend(c, 4, 66, lens, [66, 33, 5], window=window, strided=page == 16)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,Lq", [(1, 16), (1, 17), (17, 1), (1, 127), (2, 64), (1, 129), (8, 32), (1, 257), (3, 129)])
+def test_block_boundaries(D, G, Lq):
+    """Rows at the sizes where blocks and their halves fill up, over one tile of keys and more."""
+    lens = [Lq, Lq + 140]
+    c = Cache(2, 1, D, 16, lens, seed=D + Lq)
+    attend(c, G, Lq, lens)
+
+
+def test_one_workspace_for_calls_of_every_kind():
+    """Calls of different head dimensions and row counts take one workspace in turn: what one leaves in it
+    must not look like another's state."""
+    kinds = []
+    for D, G, Lq, lens in [(64, 8, 1, [3000, 40]), (128, 4, 40, [1500, 300]), (64, 4, 90, [1200, 800]), (256, 1, 60, [900, 70]),
+                           (128, 16, 1, [2500, 2500]), (256, 8, 1, [1800, 10]), (64, 16, 1, [2222, 1111])]:
+        c = Cache(2, 1, D, 16, lens, seed=D + Lq)
+        q = ref.bf16(c.rng.standard_normal((2, G, Lq, D)))
+        dev, qd, kv = c.device(), q.to(DEV), i32(lens)
+        o, lse = attend(c, G, Lq, lens, q=q, dev=dev)
+        kinds.append((dev, qd, kv, o, lse, fa2().fa2_cache_attn_workspace(qd, dev[0]).numel()))
+    ws = torch.zeros(max(k[-1] for k in kinds), dtype=torch.uint8, device=DEV)
+    order = np.random.default_rng(18).permutation(np.repeat(np.arange(len(kinds)), 6))
+    for i in order:
+        dev, qd, kv, o, lse, _ = kinds[i]
+        o2, lse2 = torch.full_like(o, FILL), torch.full_like(lse, FILL)
+        fa2().fa2_cache_attn(qd, *dev, kv, o2, lse2, workspace=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert fa2().fa2_cache_get_device_error() == (0, 0)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace, give the bits that each gives alone."""
+    calls = []
+    for G, Lq, D in [(8, 1, 64), (4, 60, 128)]:
+        lens = [2000, 900]
+        c = Cache(2, 2, D, 32, lens, seed=G)
+        q = ref.bf16(c.rng.standard_normal((2, 2 * G, Lq, D)))
+        dev, qd = c.device(), q.to(DEV)
+        o, lse = attend(c, G, Lq, lens, q=q, dev=dev)
+        calls.append((dev, qd, i32(lens), o, lse, fa2().fa2_cache_attn_workspace(qd, dev[0]), torch.cuda.Stream(DEV)))
+    outs = [[(torch.zeros_like(o), torch.zeros_like(lse)) for _ in range(8)] for _, _, _, o, lse, _, _ in calls]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for (dev, qd, kv, _, _, ws, stream), out in zip(calls, outs):
+            fa2().fa2_cache_attn(qd, *dev, kv, *out[i], workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for (_, _, _, o, lse, _, _), out in zip(calls, outs):
+        assert all(torch.equal(o, a) and torch.equal(lse, b) for a, b in out)
+    assert fa2().fa2_cache_get_device_error() == (0, 0)
+
+
+def test_two_graphs_with_their_own_workspaces():
+    """A step and a prompt chunk captured apart, replayed on two streams."""
+    runs = []
+    for G, Lq in [(4, 1), (4, 50)]:
+        lens = [1300, 700]
+        c = Cache(2, 1, 128, 16, lens, seed=G + Lq)
+        q = ref.bf16(c.rng.standard_normal((2, G, Lq, 128)))
+        dev, qd = c.device(), q.to(DEV)
+        o, lse = attend(c, G, Lq, lens, q=q, dev=dev)
+        o2, lse2, kv = torch.zeros_like(o), torch.zeros_like(lse), i32(lens)
+        ws = fa2().fa2_cache_attn_workspace(qd, dev[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fa2().fa2_cache_attn(qd, *dev, kv, o2, lse2, workspace=ws)
+        runs.append((graph, torch.cuda.Stream(DEV), o, lse, o2, lse2, dev, qd, kv, ws))
+    for _ in range(5):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, o, lse, o2, lse2, *_ in runs:
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+            o2.zero_(), lse2.zero_()
+        torch.cuda.synchronize()
+    assert fa2().fa2_cache_get_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("Lq", [1, 30])
+def test_a_padded_batch(Lq):
+    """Sequences that only pad the batch: no length, no pages, no query rows (or rows that see nothing)."""
+    lens = [200, 0, 90, 0, 0]
+    c = Cache(5, 2, 128, 16, lens, seed=19 + Lq)
+    attend(c, 4, Lq, lens, [Lq, 0, Lq, Lq, 0])
+    c.table[1] = c.table[3] = 2 ** 31 - 1
+    attend(c, 4, Lq, [200, 50, 90, 50, 0], [Lq, Lq, Lq, Lq, 0])
+
+
+def test_sizes_past_an_int_are_not_cut_off():
+    lens = [50, 20]
+    c = Cache(2, 1, 64, 16, lens, seed=20)
+    q = ref.bf16(c.rng.standard_normal((2, 4, 1, 64)))
+    o, lse = attend(c, 4, 1, lens, q=q)
+    o2, lse2 = attend(c, 4, 1, lens, q=q, window=2 ** 32 + 1, check=False)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    dev = c.device()
+    for window in (-2, -2 ** 32):
+        with pytest.raises(RuntimeError, match="FA2_ERR_INVALID_ARG"):
+            fa2().fa2_cache_attn(q.to(DEV), *dev, i32(lens), o, lse, window=window)
+    many = torch.zeros(64, dtype=torch.bfloat16, device=DEV).expand(2, 1, 2 ** 32 + 1, 64)
+    with pytest.raises(ValueError):
+        fa2().fa2_cache_write(many, many, *dev, i32([0, 0]))
+    with pytest.raises(ValueError):
+        fa2().fa2_cache_attn(many, *dev, i32(lens), many, lse)
