@@ -28,6 +28,14 @@
 //     1 warp         issues the products: one 128-row tile's run under the other's softmax
 //     1 warp         pages into shared memory by TMA
 // on one CTA an SM.  Work is cut and merged as in fa2_cache_line.cuh.
+// Measured: 2048 tokens at the end of 16384, 32 heads on 8 of 128: 515 GFLOP in 385 us, 1340
+// TFLOP/s, 69 % of the measured bf16 rate, the tensor pipe busy for 57 % of the cycles; no
+// unit is saturated (issue slots 49 %): a row tile's chain of products, scores, exponentials
+// and weights, 1500 cycles of softmax and 1400 of products, has only the other tile's to hide
+// under, and tensor memory (512 columns: S and O of two tiles) has no room for a third.  With
+// two CTAs of one row tile an SM, which convert the values twice: 499 us.  One thread a row
+// instead of two: 435 us.  At D = 64 the chain is as long for half the work: six ragged
+// prompts' chunks, 24.5 GFLOP, in 58 us.
 #pragma once
 
 #include <atomic>

@@ -6,7 +6,11 @@
 // sequence, row block, head: the heads of a row block are alike, so a place on the line is
 // found among the row blocks, which the threads of a CTA share out.
 // A unit is C::UNIT_COST tiles longer on the line than it is, for what it costs to begin and
-// end one; a range that holds only of those has nothing to do with the unit.
+// end one; a range that holds only of those has nothing to do with the unit.  No range is
+// shorter than C::MIN_TILES, for more of them than that only add parts to merge.  Measured
+// (cost / least: us): ragged chunks of prompts, by rows, 2/2: 63.1, 3/2: 61.6, 4/3: 57.7,
+// 5/3: 58.5, 7/4: 58.9; ragged steps, by columns, 1/1: 75, 2/1: 71, 3/1: 69; one short
+// sequence, 3/1: 9.3, 3/2: 10.1, 3/4: 11.9.
 // Lengths are device data, so every CTA lays out the line for itself.
 #pragma once
 
@@ -18,7 +22,13 @@ namespace cache {
 
 constexpr int CHUNK = 16;                 // keys of the smallest piece; divides every page size
 // Query rows of a key/value head (Lq G) up to which they are columns of the products, in a
-// block of 8 or 16 (fa2_cache_step.cuh); more are rows, 256 a block (fa2_cache_chunk.cuh).
+// block of 8 or 16 (fa2_cache_step.cuh); more are rows, up to 256 a block
+// (fa2_cache_chunk.cuh).  Measured, in us: 16 sequences of 4000 positions, 8 heads of 128:
+// columns 49 for 16 rows, 80 for 32 (two blocks), 137 for 64; rows 70 for any of them.
+// 24 of 2000, 2 heads of 64: 22, 27, 39 against 27; 8 of 2000, 8 heads of 256: 33, 47, 76
+// against 49.  (Two short sequences stay ahead as columns: 18 against 25 for 32 and 64 rows.
+// How long they are the host does not know.)  A block of 8 rather than 16 for up to 8 rows:
+// 41 against 45 at 16 sequences of 6000, 8 heads of 64; alike or 2 us ahead elsewhere.
 constexpr long long kStepRows = 16;
 
 // Parts of cut units: for each CTA two slots (its range's first unit, its last one) of

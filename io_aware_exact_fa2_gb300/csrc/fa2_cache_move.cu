@@ -1,7 +1,10 @@
 // fa2_cache_move.cu -- fa2_cache_write and fa2_cache_read: bf16 rows into and out of
 // the paged e4m3 cache.  Both only move bytes (3 per value: 2 bf16, 1 code); a code
 // and its scale determine the value exactly, so nothing here rounds but the one
-// conversion to e4m3.
+// conversion to e4m3.  Measured: eight prompts of up to 8192 rows, 8 heads of 128, 302 MB
+// in 46 us, 6.6 TB/s; four contexts of 16384, 16 heads of 128, 805 MB out in 122 us, 6.6
+// TB/s: the measured copy rate but for 2 %.  One row a sequence (128 of them, part
+// of a page each) and short prefixes are launches: 3.1 us.
 #include <climits>
 
 #include "fa2_cache.cuh"
@@ -82,7 +85,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f)
 
 // One block quantises one page's new rows of one head, keys or values: the page's
 // scale needs the largest magnitude of them all, so they are read once into registers
-// (NP rows a thread, 16 values of each), reduced, and written out as codes.
+// (NP rows a thread, 16 values of each), reduced, and written out as codes.  (The arithmetic
+// shows: with a magnitude compared and a code converted at a time 302 MB took 16 % more.)
 template <int T, int NP>
 __global__ void __launch_bounds__(T) write_kernel(const MoveArgs a, const int touched, const int lpr_shift)
 {
@@ -267,20 +271,24 @@ fa2_status launch_write(const MoveArgs &a, cudaStream_t stream)
     const long long blocks = 2ll * a.c.B * a.c.H * touched;
     if (blocks > INT_MAX)
         return FA2_ERR_INVALID_ARG;
-    const int threads = (a.L < page_size ? a.L : page_size) << lpr_shift;   // of 16 values each
-    if (threads <= 32)
+    // A page's rows in pieces of 16 values, four a thread where there are enough: in flight
+    // together they hide each other's latency, and short blocks the next one's.  (Half a
+    // million rows of 64, 134 MB: pages of 64 41 us with one piece, 29 with four, 31 with
+    // eight; 75 with 512 threads.)
+    const int pieces = (a.L < page_size ? a.L : page_size) << lpr_shift;
+    if (pieces <= 32)
         return run_write<32, 1>(a, blocks, touched, lpr_shift, stream);
-    if (threads <= 64)
-        return run_write<64, 1>(a, blocks, touched, lpr_shift, stream);
-    if (threads <= 128)
-        return run_write<128, 1>(a, blocks, touched, lpr_shift, stream);
-    if (threads <= 256)
-        return run_write<256, 1>(a, blocks, touched, lpr_shift, stream);
-    if (threads <= 512)
-        return run_write<256, 2>(a, blocks, touched, lpr_shift, stream);
-    if (threads <= 1024)
+    if (pieces <= 64)
+        return run_write<32, 2>(a, blocks, touched, lpr_shift, stream);
+    if (pieces <= 128)
+        return run_write<32, 4>(a, blocks, touched, lpr_shift, stream);
+    if (pieces <= 256)
+        return run_write<64, 4>(a, blocks, touched, lpr_shift, stream);
+    if (pieces <= 512)
+        return run_write<128, 4>(a, blocks, touched, lpr_shift, stream);
+    if (pieces <= 1024)
         return run_write<256, 4>(a, blocks, touched, lpr_shift, stream);
-    return run_write<256, 8>(a, blocks, touched, lpr_shift, stream);
+    return run_write<512, 4>(a, blocks, touched, lpr_shift, stream);
 }
 
 fa2_status launch_read(const MoveArgs &a, cudaStream_t stream)

@@ -29,8 +29,15 @@
 // not touched by the threads at all: TMA puts pages of 128 keys into a ring of
 // shared-memory slots, one thread issues the products, and 128 threads do the softmax of
 // R columns; the copies run ahead by the ring's depth.  Two or three CTAs share an SM, so
-// that one's softmax runs under the other's products.  Work is cut and merged as in
-// fa2_cache_line.cuh.
+// that one's softmax runs under the other's products (D = 128, 16 rows, 131 MB of cache: 49
+// us, 61 with one; D = 64, 8 rows: 41 with three, 43 with two).  Work is cut and merged as
+// in fa2_cache_line.cuh.
+// Measured: one token of 48 sequences of 64 to 8192 positions, 8 heads of 128, groups of 4:
+// 407 MB in 69 us, 5.9 TB/s, 88 % of the measured copy rate; of two of 125000: 514 MB in 86
+// us, 6.0 TB/s.  At D = 64 a tile holds half the bytes for the same softmax, and that bounds
+// it: 16 sequences of 6000, 8 heads, 98 MB in some 37 us.  Short calls are latency: of 14 us
+// for 34 MB (a window of 1024 in 16 sequences), 2 go to the launch, 1.5 to laying out the
+// line, 1 to q, 2 to merging parts.
 #pragma once
 
 #include <atomic>
