@@ -35,7 +35,7 @@
 // under, and tensor memory (512 columns: S and O of two tiles) has no room for a third.  With
 // two CTAs of one row tile an SM, which convert the values twice: 499 us.  One thread a row
 // instead of two: 435 us.  At D = 64 the chain is as long for half the work: six ragged
-// prompts' chunks, 24.5 GFLOP, in 58 us.
+// prompts' chunks, 24.5 GFLOP, in 56 us.
 #pragma once
 
 #include <atomic>
@@ -89,14 +89,18 @@ struct ChunkCfg {
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // 1024: operand alignment
     static_assert(VS + VB / 2 <= 4, "the rings hold the tiles under way");
 
-    static constexpr int TM_S = 0, TM_O = NQ * TILE;
+    // The weights lie over the scores at D = 128, where they fill tensor memory with O; else
+    // beside them, and a tile's scores are computed before the product of the one before
+    // (ragged chunks at D = 64 56.3 us, over the scores 58.0).
+    static constexpr bool P_APART = D != 128;
+    static constexpr int TM_S = 0, TM_O = NQ * TILE, TM_P = P_APART ? TM_O + NQ * D : TM_S, P_STEP = P_APART ? TILE / 2 : TILE;
     static constexpr int TMEM_COLS = 512;
     // kind::f16 with f16 A and B (formats 0), fp32 accumulator
     static constexpr uint32_t idesc(int n, bool b_mn)
     {
         return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
     }
-    static_assert(SMEM_BYTES + 1024 + 1024 <= 228 * 1024 && NQ * (TILE + D) <= TMEM_COLS, "an SM holds it");
+    static_assert(SMEM_BYTES + 1024 + 1024 <= 228 * 1024 && NQ * (TILE + D + (P_APART ? P_STEP : 0)) <= TMEM_COLS, "an SM holds it");
 };
 
 // Error codes of waits that ran out (bits 8-11 the waiting role).
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t buf = (2 * g + half) % C::VB;
                         const uint64_t dv = desc_v + (buf * C::V_BYTES >> 4);
-                        const uint32_t p = tmem + C::TM_S + q * TILE + half * (C::HALF / 2);
+                        const uint32_t p = tmem + C::TM_P + q * C::P_STEP + half * (C::HALF / 2);
 #pragma unroll
                         for (int kk = 0; kk < C::HALF / 16; ++kk)
                             mma_ts(tmem + C::TM_O + q * D, p + kk * 8, dv + (kk * 16 * 128 >> 4), C::idesc(D, true),
@@ -294,8 +298,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                                 wait(C::BAR_P_FULL + q, (done[q] + j) & 1);
                                 if (ok) {
                                     tc_fence_after();
+                                    if (C::P_APART && j + 1 < n)
+                                        issue_s(q, it + j + 1, q == nq - 1, j + 2 == n);
                                     issue_pv(q, it + j, j == 0, q == nq - 1);
-                                    if (j + 1 < n)
+                                    if (!C::P_APART && j + 1 < n)
                                         issue_s(q, it + j + 1, q == nq - 1, j + 2 == n);
                                 }
                             }
@@ -490,7 +496,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         const int rt = warp >> 3, row = tid & 127, half = warp >> 2 & 1;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float scale_log2 = a.scale * 1.4426950408889634f;
-        const uint32_t o_addr = tmem + lanes + C::TM_O + rt * D, s_addr = tmem + lanes + C::TM_S + rt * TILE;
+        const uint32_t o_addr = tmem + lanes + C::TM_O + rt * D, s_addr = tmem + lanes + C::TM_S + rt * TILE,
+                       p_addr = tmem + lanes + C::TM_P + rt * C::P_STEP;
         auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + rt) : "memory"); };   // the row tile's warps
         // the two warps of the same rows
         const int pair_id = 3 + rt * 4 + (warp & 3);
@@ -714,20 +721,20 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         sum += sum0 + sum1;
                         add_l = fmaf(sum0 + sum1, lf, add_l);
                     });
-                    // (f16 ends at 65504; by the tile's own maximum the sum is 2^12 at most.)  The
-                    // weights go over the scores, so both threads have read theirs after this.
+                    // (f16 ends at 65504; by the tile's own maximum the sum is 2^12 at most.)  Both
+                    // threads have read their scores after this, which the weights may go over.
                     again = pair_any(sum > 32768.f);
                     if (!again)
                         break;
                 }
                 l += add_l;
-                // A parity tells a phase from the one before only, so the wait for the last
-                // tile's product (below) needs that for the last but one's, before the last can
-                // complete.
-                if (!waited && j == n - 1)
+                // Weights apart go where the tile before's were.  Weights over the scores: the
+                // products that made these came after its; but a parity tells a phase from the
+                // one before only, so the wait for the last tile's product (below) needs that
+                // for the last but one's, before the last can complete.
+                if (!waited && (C::P_APART || j == n - 1))
                     wait(C::BAR_O_DONE + rt, (d - 1) & 1);
-                // over the first half of S
-                tmem_st32(s_addr + half * 32, p);
+                tmem_st32(p_addr + half * 32, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(C::BAR_P_FULL + rt);
