@@ -28,14 +28,14 @@
 //     1 warp         issues the products: one 128-row tile's run under the other's softmax
 //     1 warp         pages into shared memory by TMA
 // on one CTA an SM.  Work is cut and merged as in fa2_cache_line.cuh.
-// Measured: 2048 tokens at the end of 16384, 32 heads on 8 of 128: 515 GFLOP in 385 us, 1340
+// Measured: 2048 tokens at the end of 16384, 32 heads on 8 of 128: 515 GFLOP in 382 us, 1350
 // TFLOP/s, 69 % of the measured bf16 rate, the tensor pipe busy for 57 % of the cycles; no
 // unit is saturated (issue slots 49 %): a row tile's chain of products, scores, exponentials
 // and weights, 1500 cycles of softmax and 1400 of products, has only the other tile's to hide
 // under, and tensor memory (512 columns: S and O of two tiles) has no room for a third.  With
 // two CTAs of one row tile an SM, which convert the values twice: 499 us.  One thread a row
 // instead of two: 435 us.  At D = 64 the chain is as long for half the work: six ragged
-// prompts' chunks, 24.5 GFLOP, in 56 us.
+// prompts' chunks, 24.5 GFLOP, in 55 us.
 #pragma once
 
 #include <atomic>
@@ -66,32 +66,37 @@ struct ChunkCfg {
 
     static constexpr int ROW = D == 64 ? 64 : 128;   // bytes of a row of codes: its swizzle span
     static constexpr int PANELS = D / ROW, PANEL = TILE * ROW;       // of a stage of codes
-    static constexpr int STAGE = TILE * D, KS = D == 256 ? 1 : 2, VS = D == 256 ? 1 : 2;   // stages of keys, of values
+    static constexpr int STAGE = TILE * D;
+    // Stages of keys, of values: as many as there is room for.  (What is loaded when a stage
+    // comes free takes 2 us from memory; D = 64, 32 rows, 98 MB of cache: 57 us, 63 with two.)
+    static constexpr int KS = D == 64 ? 4 : D == 128 ? 2 : 1, VS = KS;
     static constexpr int Q_PANEL = 128 * ROW, Q_TERM = 128 * D, Q_TILE = 2 * Q_TERM;   // Q: two terms of codes a row tile
     // V in f16, half a tile's keys a buffer: panels of 64 columns, 128-byte rows
     static constexpr int HALF = TILE / 2, V_PANEL = HALF * 128, V_BYTES = HALF * D * 2, VB = D == 256 ? 2 : 4;
     static constexpr int OFF_Q = 0, OFF_V = NQ * Q_TILE, OFF_K = OFF_V + VB * V_BYTES, OFF_RAW = OFF_K + KS * STAGE;
-    // Rings of four tiles: group scales, NaN flags, NaN values by key.  (Tile g is loaded when
-    // the values of g - VS have been read, which waits for the products of g - VS - VB / 2.)
+    // Rings of tiles: group scales of eight; NaN flags, NaN values by key of four.  (Tile g is
+    // loaded when the values of g - VS have been read, which waits for the products of g - VS -
+    // VB / 2.)
     static constexpr int NAN_WORDS = D / 32;
-    static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16;
-    static constexpr int OFF_FLAGS = OFF_INFO + 4 * INFO_BYTES;
+    static constexpr int OFF_INFO = OFF_RAW + VS * STAGE, INFO_BYTES = GROUPS * 16 + 16, RING = 8;
+    static constexpr int OFF_FLAGS = OFF_INFO + RING * INFO_BYTES;
     static constexpr int OFF_NAN = OFF_FLAGS + 16, NAN_BYTES = TILE * NAN_WORDS * 4;
     static constexpr int OFF_MARK = OFF_NAN + 4 * NAN_BYTES;         // values of O that are NaN, by row
     static constexpr int OFF_PAIR = OFF_MARK + R * NAN_WORDS * 4;    // a float of each softmax thread
-    static constexpr int OFF_BAR = OFF_PAIR + 2 * R * 4;
-    // (the first six: one for each row tile)
-    static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 2, BAR_S_FULL = 4, BAR_P_FULL = 6, BAR_O_DONE = 8, BAR_O_FREE = 10,
-                         BAR_DRAIN = 12, BAR_V_FULL = 13, BAR_V_EMPTY = BAR_V_FULL + VB, BAR_K_FULL = BAR_V_EMPTY + VB,
+    static constexpr int OFF_SUM = OFF_PAIR + 2 * R * 4;             // maximum and sum of a row, by row tile
+    static constexpr int OFF_BAR = OFF_SUM + R * 8;
+    // (the first five: one for each row tile)
+    static constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 2, BAR_S_FULL = 4, BAR_P_FULL = 6, BAR_O_DONE = 8, BAR_DRAIN = 10,
+                         BAR_V_FULL = 11, BAR_V_EMPTY = BAR_V_FULL + VB, BAR_K_FULL = BAR_V_EMPTY + VB,
                          BAR_K_EMPTY = BAR_K_FULL + KS, BAR_RAW_FULL = BAR_K_EMPTY + KS, BAR_RAW_EMPTY = BAR_RAW_FULL + VS,
                          NUM_BAR = BAR_RAW_EMPTY + VS;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // 1024: operand alignment
-    static_assert(VS + VB / 2 <= 4, "the rings hold the tiles under way");
+    static_assert(VS + VB / 2 <= RING && VB / 2 + 1 <= 4, "the rings hold the tiles under way");
 
     // The weights lie over the scores at D = 128, where they fill tensor memory with O; else
     // beside them, and a tile's scores are computed before the product of the one before
-    // (ragged chunks at D = 64 56.3 us, over the scores 58.0).
+    // (ragged chunks at D = 64: 3 % off the call).
     static constexpr bool P_APART = D != 128;
     static constexpr int TM_S = 0, TM_O = NQ * TILE, TM_P = P_APART ? TM_O + NQ * D : TM_S, P_STEP = P_APART ? TILE / 2 : TILE;
     static constexpr int TMEM_COLS = 512;
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
     if (tid == 0) {
         for (int i = 0; i < C::NUM_BAR; ++i) {
-            const bool rows = i / 2 == C::BAR_Q_FULL / 2 || i / 2 == C::BAR_P_FULL / 2 || i / 2 == C::BAR_O_FREE / 2;
+            const bool rows = i / 2 == C::BAR_Q_FULL / 2 || i / 2 == C::BAR_P_FULL / 2;
             const bool convert = (i >= C::BAR_V_FULL && i < C::BAR_V_EMPTY) || i >= C::BAR_RAW_EMPTY;
             mbar_init(bar(i), rows ? 8 : convert ? 4 : 1);
         }
@@ -205,13 +210,16 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     };
     // what the loading warp says of tile g: a group's scales, and whether every row sees every key
     auto group_word = [](const uint8_t *smem, uint32_t g, int q) {
-        return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES)[q * 4 + 3];
+        return reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + g % C::RING * C::INFO_BYTES)[q * 4 + 3];
     };
     auto is_whole = [](const uint8_t *smem, uint32_t g) {
-        return *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES + GROUPS * 16) != 0;
+        return *reinterpret_cast<const uint32_t *>(smem + C::OFF_INFO + g % C::RING * C::INFO_BYTES + GROUPS * 16) != 0;
     };
     uint32_t it = 0;               // tiles before the present unit's first
-    auto row_tiles = [&] { return C::NQ > 1 && line.s.n * a.G - line.rb * R > 128 ? 2 : 1; };
+    // A unit of no more than 128 rows: the row tiles are the same rows, one with the even
+    // tiles of keys, one with the odd ones, and are put together at the end.  (32 rows, 131 MB
+    // of cache, D = 128: 61 us, 70 with one row tile idle.)
+    auto is_twin = [&] { return C::NQ > 1 && line.s.n * a.G - line.rb * R <= 128; };
 
     if (warp >= C::WARP_MMA) {
         // ============================================ one thread issues the products
@@ -229,10 +237,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     if (ok)
                         ok = lone_wait(bar(i), parity, a.err, CHUNK_ERR_MMA | i, limit);
                 };
-                // S = Q K^T of row tile q and tile g of keys; of them all the last to read the tile
-                auto issue_s = [&](int q, uint32_t g, bool last_q, bool last_g) {
+                // S = Q K^T of row tile q (rows q_at of Q) and tile g of keys, the last to read
+                // this tile of keys, of Q
+                auto issue_s = [&](int q, int q_at, uint32_t g, bool last_k, bool last_q) {
                     const uint32_t stage = g % C::KS;
-                    const uint64_t dk = desc_k + (stage * C::STAGE >> 4), dq = desc_q + (q * C::Q_TILE >> 4);
+                    const uint64_t dk = desc_k + (stage * C::STAGE >> 4), dq = desc_q + (q_at * C::Q_TILE >> 4);
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -243,12 +252,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                                          term > 0 || kk > 0);
                         }
                     mma_commit(bar(C::BAR_S_FULL + q));
-                    if (last_q)
+                    if (last_k)
                         mma_commit(bar(C::BAR_K_EMPTY + stage));
-                    if (last_g)
-                        mma_commit(bar(C::BAR_Q_EMPTY + q));
+                    if (last_q)
+                        mma_commit(bar(C::BAR_Q_EMPTY + q_at));
                 };
-                auto issue_pv = [&](int q, uint32_t g, bool start, bool last_q) {   // O += P V
+                auto issue_pv = [&](int q, uint32_t g, bool start, bool last_v) {   // O += P V
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t buf = (2 * g + half) % C::VB;
@@ -258,61 +267,73 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         for (int kk = 0; kk < C::HALF / 16; ++kk)
                             mma_ts(tmem + C::TM_O + q * D, p + kk * 8, dv + (kk * 16 * 128 >> 4), C::idesc(D, true),
                                    !start || half > 0 || kk > 0);
-                        if (last_q)
+                        if (last_v)
                             mma_commit(bar(C::BAR_V_EMPTY + buf));
                     }
                     mma_commit(bar(C::BAR_O_DONE + q));
                 };
                 auto wait_k = [&](uint32_t g) { wait(C::BAR_K_FULL + g % C::KS, g / C::KS & 1); };
                 auto wait_v = [&](uint32_t item) { wait(C::BAR_V_FULL + item % C::VB, item / C::VB & 1); };
-                // of each row tile: tiles of keys, and units, before the present unit
-                uint32_t done[C::NQ] = {}, units[C::NQ] = {};
+                // of each row tile: tiles of keys, and loads of Q, before the present unit
+                uint32_t done[C::NQ] = {}, loads[C::NQ] = {};
                 bool more;
                 do {
                     int tile0, tile1;
                     part_of(tile0, tile1);
-                    const int n = tile1 - tile0, nq = row_tiles();
+                    const int n = tile1 - tile0;
+                    const bool twin = is_twin();
+                    // The first tiles' scores; then for each tile and row tile the product with the
+                    // values, and the scores of the tile after.  What the first of these reads
+                    // beside the weights is waited for before them: they go out in one run.  (A
+                    // unit's first product overwrites O: the warps whose weights it waits for
+                    // have read out the one before.)
                     wait_k(it);
+                    if (twin && n > 1)
+                        wait_k(it + 1);
 #pragma unroll
-                    for (int q = 0; q < C::NQ; ++q)
-                        if (q < nq) {
-                            wait(C::BAR_Q_FULL + q, units[q] & 1);
-                            if (ok) {
-                                tc_fence_after();
-                                issue_s(q, it, q == nq - 1, n == 1);
-                            }
+                    for (int q = 0; q < C::NQ; ++q) {
+                        if (q == 0 || !twin)
+                            wait(C::BAR_Q_FULL + q, loads[q] & 1);
+                        if (ok && (q == 0 || !twin || n > 1)) {
+                            tc_fence_after();
+                            if (twin)
+                                issue_s(q, 0, it + q, true, n <= q + 1);
+                            else
+                                issue_s(q, q, it, q == C::NQ - 1, n == 1);
                         }
+                    }
+                    const int ahead = twin ? 2 : 1;
                     for (int j = 0; j < n && ok; ++j) {
-                        // (keys and values first: when the weights are there, this tile's and
-                        // the next one's products go out in one run)
                         wait_v(2 * (it + j));
                         wait_v(2 * (it + j) + 1);
-                        if (j + 1 < n)
-                            wait_k(it + j + 1);
+                        if (C::P_APART && j + ahead < n)
+                            wait_k(it + j + ahead);
 #pragma unroll
                         for (int q = 0; q < C::NQ; ++q)
-                            if (q < nq) {
-                                // a unit's first product overwrites O: the one before has been read out
-                                if (j == 0 && units[q] > 0)
-                                    wait(C::BAR_O_FREE + q, (units[q] - 1) & 1);
-                                wait(C::BAR_P_FULL + q, (done[q] + j) & 1);
+                            if (!twin || q == (j & 1)) {
+                                wait(C::BAR_P_FULL + q, (done[q] + (twin ? j >> 1 : j)) & 1);
                                 if (ok) {
+                                    const bool next = j + ahead < n;
                                     tc_fence_after();
-                                    if (C::P_APART && j + 1 < n)
-                                        issue_s(q, it + j + 1, q == nq - 1, j + 2 == n);
-                                    issue_pv(q, it + j, j == 0, q == nq - 1);
-                                    if (!C::P_APART && j + 1 < n)
-                                        issue_s(q, it + j + 1, q == nq - 1, j + 2 == n);
+                                    if (C::P_APART && next)
+                                        issue_s(q, twin ? 0 : q, it + j + ahead, twin || q == C::NQ - 1, j + ahead == n - 1);
+                                    issue_pv(q, it + j, j < ahead, twin || q == C::NQ - 1);
+                                    if (!C::P_APART && next) {
+                                        wait_k(it + j + ahead);
+                                        if (!ok)
+                                            break;
+                                        tc_fence_after();
+                                        issue_s(q, twin ? 0 : q, it + j + ahead, twin || q == C::NQ - 1, j + ahead == n - 1);
+                                    }
                                 }
                             }
                     }
                     it += n;
 #pragma unroll
-                    for (int q = 0; q < C::NQ; ++q)
-                        if (q < nq) {
-                            done[q] += n;
-                            ++units[q];
-                        }
+                    for (int q = 0; q < C::NQ; ++q) {
+                        done[q] += twin ? (n + 1 - q) >> 1 : n;
+                        loads[q] += q == 0 || !twin;
+                    }
                     Line<C> &mine = sh.line[C::WARP_MMA];
                     more = ok && mine.next(a) && mine.at < sh.end;
                 } while (more);
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * box_bytes;
                     const int pos0 = from + j * TILE;
                     const bool whole = __all_sync(0xffffffffu, !mine || fine) && pos0 >= all_lo && pos0 + TILE <= all_hi;
-                    uint8_t *const to = smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES;
+                    uint8_t *const to = smem + C::OFF_INFO + g % C::RING * C::INFO_BYTES;
                     if (mine)
                         for (int k = 0; k < 1 << (box_shift - 4); ++k)
                             reinterpret_cast<float4 *>(to)[(in_tile << (box_shift - 4)) + k] = info;
@@ -498,7 +519,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         const float scale_log2 = a.scale * 1.4426950408889634f;
         const uint32_t o_addr = tmem + lanes + C::TM_O + rt * D, s_addr = tmem + lanes + C::TM_S + rt * TILE,
                        p_addr = tmem + lanes + C::TM_P + rt * C::P_STEP;
-        auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + rt) : "memory"); };   // the row tile's warps
+        // the row tile's warps; all of them
+        auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + rt) : "memory"); };
+        auto all_sync = [] { asm volatile("bar.sync 11, %0;" ::"n"(256 * C::NQ) : "memory"); };
         // the two warps of the same rows
         const int pair_id = 3 + rt * 4 + (warp & 3);
         auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory"); };
@@ -519,17 +542,16 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             if (ok)
                 ok = warp_wait(i, parity, CHUNK_ERR_SOFTMAX);
         };
-        uint32_t n_done = 0, unit = 0;                         // of this row tile
+        uint32_t n_done = 0, loads = 0;                        // of this row tile: tiles of keys, and loads of Q
         do {
             int tile0, tile1;
             part_of(tile0, tile1);
             const int n = tile1 - tile0;
-            if (rt >= row_tiles()) {
-                it += n;
-                continue;
-            }
+            const bool twin = is_twin();
+            const int every = twin ? 2 : 1, j0 = twin ? rt : 0;   // this row tile's tiles of keys
+            const int row_at = twin ? row : rt * 128 + row;       // its row in the unit
             const int from = (line.span.lo & ~(C::ALIGN - 1)) + tile0 * TILE;
-            const int rr = line.rb * R + rt * 128 + row;
+            const int rr = line.rb * R + row_at;
             const bool live = rr < line.s.n * a.G;
             const int tok = rr / a.G, hq = line.h * a.G + rr % a.G;
             int lo = 0, hi = 0;                                  // keys the row sees
@@ -566,30 +588,34 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 e = e < -126 ? -126 : e;
                 // a row with an infinity or NaN has no finite scores: make it NaN
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
-                if (unit > 0)
-                    wait(C::BAR_Q_EMPTY + rt, (unit - 1) & 1);
+                const bool loads_q = !twin || rt == 0;
+                if (loads_q && loads > 0)
+                    wait(C::BAR_Q_EMPTY + rt, (loads - 1) & 1);
+                if (loads_q) {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t t0[4], t1[4];
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t t0[4], t1[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w[4] = {x[c * 2 + i].x, x[c * 2 + i].y, x[c * 2 + i].z, x[c * 2 + i].w};
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t w[4] = {x[c * 2 + i].x, x[c * 2 + i].y, x[c * 2 + i].z, x[c * 2 + i].w};
 #pragma unroll
-                        for (int k = 0; k < 4; k += 2) {
-                            uint32_t y0 = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-                            uint32_t y1 = pack_f16x2(__uint_as_float(w[k + 1] << 16) * f, __uint_as_float(w[k + 1] & 0xffff0000u) * f);
-                            t0[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
-                            t1[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                            for (int k = 0; k < 4; k += 2) {
+                                uint32_t y0 = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+                                uint32_t y1 = pack_f16x2(__uint_as_float(w[k + 1] << 16) * f, __uint_as_float(w[k + 1] & 0xffff0000u) * f);
+                                t0[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                                t1[i * 2 + k / 2] = take_term<1>(y0) | take_term<1>(y1) << 16;
+                            }
                         }
+                        const int col = half * (D / 32) + c, panel = col * 16 / C::ROW, swizzle = C::ROW == 64 ? row >> 1 & 3 : row & 7;
+                        const uint32_t at = base + C::OFF_Q + rt * C::Q_TILE + panel * C::Q_PANEL + row * C::ROW +
+                                            ((col % (C::ROW / 16) ^ swizzle) << 4);
+                        st_shared_v4(at, t0[0], t0[1], t0[2], t0[3]);
+                        st_shared_v4(at + C::Q_TERM, t1[0], t1[1], t1[2], t1[3]);
                     }
-                    const int col = half * (D / 32) + c, panel = col * 16 / C::ROW, swizzle = C::ROW == 64 ? row >> 1 & 3 : row & 7;
-                    const uint32_t at = base + C::OFF_Q + rt * C::Q_TILE + panel * C::Q_PANEL + row * C::ROW +
-                                        ((col % (C::ROW / 16) ^ swizzle) << 4);
-                    st_shared_v4(at, t0[0], t0[1], t0[2], t0[3]);
-                    st_shared_v4(at + C::Q_TERM, t1[0], t1[1], t1[2], t1[3]);
+                    fence_proxy_async_shared();
+                    warp_arrive(C::BAR_Q_FULL + rt);
+                    ++loads;
                 }
-                fence_proxy_async_shared();
-                warp_arrive(C::BAR_Q_FULL + rt);
             }
 
             const float scale_row = scale_log2 * pow2i(e);
@@ -600,11 +626,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 #pragma unroll
                 for (int w = 0; w < C::NAN_WORDS; ++w)
                     mark[w * R] = 0;
-            for (int j = 0; j < n; ++j) {
-                const uint32_t g = it + j, d = n_done + j;
+            for (int j = j0; j < n; j += every) {
+                const uint32_t g = it + j, d = n_done + (twin ? j >> 1 : j);
+                const bool fresh = j < every, last = j + every >= n;   // the first of them, the last
                 wait(C::BAR_S_FULL + rt, d & 1);
                 tc_fence_after();
-                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + (g & 3) * C::INFO_BYTES);
+                const float4 *const info = reinterpret_cast<const float4 *>(smem + C::OFF_INFO + g % C::RING * C::INFO_BYTES);
                 const int pos0 = from + j * TILE;
                 const bool whole = is_whole(smem, g);
                 if (!whole) {            // NaN values, once the tile's are converted
@@ -661,7 +688,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // taken, O and l brought to it, and the weights taken again.
                 uint32_t p[32];
                 float sum, add_l;
-                bool waited = j == 0;
+                bool waited = fresh;
                 bool again = __any_sync(0xffffffffu, M == -INFINITY && lo < pos0 + TILE && hi > pos0);
                 for (int attempt = 0; attempt < 2; ++attempt) {
                     if (again) {
@@ -683,7 +710,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             M = top;
                             l *= f;
                         }
-                        if (j > 0) {             // O in tensor memory stands for the old maximum
+                        if (!fresh) {            // O in tensor memory stands for the old maximum
                             if (!waited)
                                 wait(C::BAR_O_DONE + rt, (d - 1) & 1);
                             waited = true;
@@ -732,7 +759,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // products that made these came after its; but a parity tells a phase from the
                 // one before only, so the wait for the last tile's product (below) needs that
                 // for the last but one's, before the last can complete.
-                if (!waited && (C::P_APART || j == n - 1))
+                if (!waited && (C::P_APART || last))
                     wait(C::BAR_O_DONE + rt, (d - 1) & 1);
                 tmem_st32(p_addr + half * 32, p);
                 tmem_st_wait();
@@ -742,11 +769,28 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
 
             // ---- O out of tensor memory: the unit's rows, or this part of them
             it += n;
-            n_done += n;
+            const int mine = twin ? (n + 1 - rt) >> 1 : n;
+            n_done += mine;
             pair[tid] = l;
             pair_sync();
             l = (half ? pair[tid ^ 128] : l) + (half ? l : pair[tid ^ 128]);   // (in one order)
-            wait(C::BAR_O_DONE + rt, (n_done - 1) & 1);
+            if (mine > 0)
+                wait(C::BAR_O_DONE + rt, (n_done - 1) & 1);
+            // Twins: both tiles' maxima and sums; each tile's warps then take half of the columns.
+            float f0 = 1.f, f1 = 0.f;
+            if (twin) {
+                float2 *const sums = reinterpret_cast<float2 *>(smem + C::OFF_SUM) + row;
+                if (half == 0)
+                    sums[rt * 128] = make_float2(M, l);
+                tc_fence_before();
+                all_sync();
+                const float2 x = sums[0], y = sums[128];
+                M = fmaxf(x.x, y.x);
+                const float ref = M == -INFINITY ? 0.f : M;
+                f0 = ex2_approx(x.x - ref);
+                f1 = ex2_approx(y.x - ref);
+                l = x.y * f0 + y.y * f1;
+            }
             tc_fence_after();
             const int first_cta = cut ? sh.range.owner(line.at) : cta;
             const int last_cta = cut ? sh.range.owner(line.at + line.span.tiles - 1) : cta;
@@ -757,14 +801,31 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             float *const part =
                 cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
             // a part's quadruple u of columns: neighbouring threads' rows lie next to each other
-            auto place = [&](int u) { return (u * R + rt * 128 + row) * 4; };
+            auto place = [&](int u) { return (u * R + row_at) * 4; };
+            const int chunk0 = twin ? rt * 2 + half : half, chunks = twin ? 4 : 2;   // of 16 columns: the first, every
 #pragma unroll 1
-            for (int cc = half * (D / 32); cc < (half + 1) * (D / 32); ++cc) {   // 16 columns
+            for (int cc = chunk0; cc < D / 16; cc += chunks) {
                 uint32_t r[16];
-                tmem_ld(o_addr + 16 * cc, r);
+                tmem_ld((twin ? o_addr - rt * D : o_addr) + 16 * cc, r);
                 tmem_wait_ld();
                 tmem_pin(r);
-                const uint32_t marked = mark[(cc >> 1) * R] >> (cc & 1) * 16;
+                uint32_t marked = mark[(cc >> 1) * R];
+                if (twin) {
+                    marked |= mark[(cc >> 1) * R + (rt ? -128 : 128)];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        r[k] = __float_as_uint(__uint_as_float(r[k]) * f0);
+                    if (n > 1) {
+                        uint32_t r1[16];
+                        tmem_ld(o_addr + (1 - rt) * D + 16 * cc, r1);
+                        tmem_wait_ld();
+                        tmem_pin(r1);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            r[k] = __float_as_uint(fmaf(__uint_as_float(r1[k]), f1, __uint_as_float(r[k])));
+                    }
+                }
+                marked >>= (cc & 1) * 16;
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     r[k] = (marked >> k & 1) ? 0x7fc00000u : __float_as_uint(__uint_as_float(r[k]) * inv);
@@ -783,34 +844,41 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 }
             }
             tc_fence_before();
-            warp_arrive(C::BAR_O_FREE + rt);
             auto write_lse = [&](float v) {
                 a.lse[(static_cast<long long>(line.b) * a.Hq + hq) * a.Lq + tok] = v * 0.69314718055994531f;
             };
             if (alone) {
-                if (half == 0 && live)
+                if (chunk0 == 0 && live)
                     write_lse(lse2);
             } else {
-                if (half == 0)
-                    part[R * D + rt * 128 + row] = lse2;
+                if (chunk0 == 0)
+                    part[R * D + row_at] = lse2;
                 // the CTA whose part is the last to arrive merges them, each row tile by itself
+                // (twins together)
+                auto sync = [&] {
+                    if (twin)
+                        all_sync();
+                    else
+                        tile_sync();
+                };
                 __threadfence();
-                tile_sync();
-                volatile int *const last = reinterpret_cast<int *>(smem + C::OFF_MISC + 4) + rt;
-                if ((tid & 255) == 0) {
-                    int *const counter = parts.counters + 2 * first_cta + rt;
+                sync();
+                const int tile = twin ? 0 : rt;
+                volatile int *const last = reinterpret_cast<int *>(smem + C::OFF_MISC + 4) + tile;
+                if ((tid & 255) == 0 && rt == tile) {
+                    int *const counter = parts.counters + 2 * first_cta + tile;
                     *last = atomicAdd(counter, 1) == last_cta - first_cta;
                     if (*last)
                         *counter = 0;
                 }
-                tile_sync();
+                sync();
                 if (*last) {
                     __threadfence();
 #pragma unroll 1
-                    for (int cc = half; cc < D / 16; cc += 2) {
+                    for (int cc = chunk0; cc < D / 16; cc += chunks) {
                         float4 v[4];
                         const float merged =
-                            merge_row<C, 4>(parts, first_cta, last_cta, rt * 128 + row, [&](int k) { return place(cc * 4 + k); }, v);
+                            merge_row<C, 4>(parts, first_cta, last_cta, row_at, [&](int k) { return place(cc * 4 + k); }, v);
                         if (live) {
 #pragma unroll
                             for (int k = 0; k < 4; k += 2)
@@ -823,8 +891,11 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     }
                 }
             }
-            ++unit;
-            pair_sync();          // (the marks are read)
+            // the marks and O are read
+            if (twin)
+                all_sync();
+            else
+                pair_sync();
         } while (next_unit());
         tmem_st_wait();   // a loop left early may leave stores in flight
     }

@@ -24,8 +24,8 @@ constexpr int CHUNK = 16;                 // keys of the smallest piece; divides
 // Query rows of a key/value head (Lq G) up to which they are columns of the products, in a
 // block of 8 or 16 (fa2_cache_step.cuh); more are rows, up to 256 a block
 // (fa2_cache_chunk.cuh).  Measured, in us: 16 sequences of 4000 positions, 8 heads of 128:
-// columns 49 for 16 rows, 80 for 32 (two blocks), 137 for 64; rows 70 for any of them.
-// 24 of 2000, 2 heads of 64: 22, 27, 39 against 27; 8 of 2000, 8 heads of 256: 33, 47, 76
+// columns 49 for 16 rows, 80 for 32 (two blocks), 137 for 64; rows 61 for any of them.
+// 24 of 2000, 2 heads of 64: 21, 27, 39 against 27; 8 of 2000, 8 heads of 256: 33, 47, 76
 // against 49.  (Two short sequences stay ahead as columns: 18 against 25 for 32 and 64 rows.
 // How long they are the host does not know.)  A block of 8 rather than 16 for up to 8 rows:
 // 41 against 45 at 16 sequences of 6000, 8 heads of 64; alike or 2 us ahead elsewhere.
