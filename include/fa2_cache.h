@@ -126,10 +126,13 @@ fa2_status fa2_cache_read(const fa2_cache *c, void *k, void *v, const long long 
  * at most 2^-21 of it (up to 16 rows, Lq * Hq / H) or 2^-17 (more).  Sums and softmax
  * are fp32; softmax weights are rounded to three e4m3 terms (12 bits; up to 16 rows)
  * or to fp16 (11 bits) for the product with V.  A row of q with an infinity or NaN
- * gives NaN.
+ * gives NaN.  Scales are those that fa2_cache_write gives, 2^-96 to 2^119, or NaN;
+ * keys whose value scale is more than 2^100 below the largest that a row sees may be
+ * missing from its sums (a page of zeros has 2^-96).
  *
  *   q          bf16 [B, Hq, Lq, D] device view, strides (batch, head, row) or NULL.
- *   o          bf16 [B, Hq, Lq, D] device view (written), likewise; rows must not overlap.
+ *   o          bf16 [B, Hq, Lq, D] device view (written), likewise; its rows must not overlap
+ *              one another, nor q.
  *   lse        fp32 [B, Hq, Lq] contiguous (written).
  *   kv_lens    int32 [B] device: positions held, the query tokens among them.
  *   q_lens     int32 [B] device, 0..Lq: query rows of each sequence; NULL: Lq for

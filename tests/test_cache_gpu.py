@@ -1,6 +1,10 @@
 """The 8-bit cache on the GPU against its definition in 64 bits (cache_reference): writing
 and reading must give the very codes, scales and values; attention is held to the bounds
 that cache_reference.attention derives."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -613,3 +617,33 @@ def test_sizes_past_an_int_are_not_cut_off():
         fa2().fa2_cache_write(many, many, *dev, i32([0, 0]))
     with pytest.raises(ValueError):
         fa2().fa2_cache_attn(many, *dev, i32(lens), many, lse)
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing that a first call sets up (kernel attributes, the error word) is missed or refused in a capture."""
+    code = """
+import torch, io_aware_exact_fa2_gb300 as f
+dev = torch.device("cuda:0")
+k = torch.ones(1, 1, 3, 64, dtype=torch.bfloat16, device=dev)
+c = [torch.zeros(2, 1, 16, 64, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+s = [torch.zeros(2, 1, dtype=torch.uint8, device=dev).view(torch.float8_e8m0fnu) for _ in range(2)]
+cache = (*c, *s, torch.tensor([[1, 0]], dtype=torch.int32, device=dev))
+start, held = torch.zeros(1, dtype=torch.int32, device=dev), torch.full((1,), 3, dtype=torch.int32, device=dev)
+back = [torch.zeros_like(k) for _ in range(2)]
+outs = [(torch.zeros(1, n, 3, 64, dtype=torch.bfloat16, device=dev), torch.zeros(1, n, 3, device=dev)) for n in (2, 8)]
+qs = [torch.ones_like(o) for o, _ in outs]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    f.fa2_cache_write(k, k, *cache, start)
+    f.fa2_cache_read(*cache, *back, start)
+    for q, (o, lse) in zip(qs, outs):
+        f.fa2_cache_attn(q, *cache, held, o, lse)
+graph.replay()
+torch.cuda.synchronize()
+assert all(bool((t == 1).all()) for t in (*back, *(o for o, _ in outs)))
+print("done")
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.returncode == 0 and out.stdout.strip().endswith("done"), out.stderr[-2000:]
