@@ -35,7 +35,7 @@
 // under, and tensor memory (512 columns: S and O of two tiles) has no room for a third.  With
 // two CTAs of one row tile an SM, which convert the values twice: 499 us.  One thread a row
 // instead of two: 435 us.  At D = 64 the chain is as long for half the work: six ragged
-// prompts' chunks, 24.5 GFLOP, in 55 us.
+// prompts' chunks, 24.5 GFLOP, in 54 us.
 #pragma once
 
 #include <atomic>
@@ -96,7 +96,7 @@ struct ChunkCfg {
 
     // The weights lie over the scores at D = 128, where they fill tensor memory with O; else
     // beside them, and a tile's scores are computed before the product of the one before
-    // (ragged chunks at D = 64: 3 % off the call).
+    // (ragged chunks at D = 64: 58.0 us over the scores, 53.6 apart).
     static constexpr bool P_APART = D != 128;
     static constexpr int TM_S = 0, TM_O = NQ * TILE, TM_P = P_APART ? TM_O + NQ * D : TM_S, P_STEP = P_APART ? TILE / 2 : TILE;
     static constexpr int TMEM_COLS = 512;
@@ -728,6 +728,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             }
                         }
                     }
+                    // weights apart go where the tile before's were, as they are made
+                    if (C::P_APART && !waited) {
+                        wait(C::BAR_O_DONE + rt, (d - 1) & 1);
+                        waited = true;
+                        tc_fence_after();
+                    }
                     const float ref = 6.f - (M == -INFINITY ? 0.f : M);
                     sum = add_l = 0.f;
                     for_groups([&](int i, const uint32_t (&r)[CHUNK], float c, float ev, float lf) {
@@ -743,6 +749,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                             sum2 = add_f32x2(sum2, f32x2(x0, x1));
                             p[i * 8 + k / 2] = pack_f16x2(x0, x1);
                         }
+                        if (C::P_APART && i % 2)
+                            tmem_st16(p_addr + half * 32 + i / 2 * 16, p + i / 2 * 16);
                         float sum0, sum1;
                         unpack_f32x2(sum2, sum0, sum1);
                         sum += sum0 + sum1;
@@ -755,13 +763,15 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         break;
                 }
                 l += add_l;
-                // Weights apart go where the tile before's were.  Weights over the scores: the
-                // products that made these came after its; but a parity tells a phase from the
-                // one before only, so the wait for the last tile's product (below) needs that
-                // for the last but one's, before the last can complete.
-                if (!waited && (C::P_APART || last))
-                    wait(C::BAR_O_DONE + rt, (d - 1) & 1);
-                tmem_st32(p_addr + half * 32, p);
+                if (!C::P_APART) {
+                    // Over the scores: the products that made these came after the tile before's.
+                    // But a parity tells a phase from the one before only, so the wait for the
+                    // last tile's product (below) needs that for the last but one's, before the
+                    // last can complete.
+                    if (!waited && last)
+                        wait(C::BAR_O_DONE + rt, (d - 1) & 1);
+                    tmem_st32(p_addr + half * 32, p);
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(C::BAR_P_FULL + rt);
