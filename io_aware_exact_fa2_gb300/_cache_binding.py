@@ -199,7 +199,8 @@ def fa2_cache_attn_workspace_size(B: int, Hq: int, H: int, Lq: int, D: int, devi
 
 def fa2_cache_attn_workspace(q, k_cache):
     """A zero-filled uint8 CUDA tensor sized for fa2_cache_attn on q's problem.  Keep it
-    between calls; calls that may overlap on the GPU need one each."""
+    between calls; calls that may overlap on the GPU need one each.  It is filled on the
+    current stream: a first call on another one has to wait for that."""
     B, Hq, Lq, D = q.shape
     n = fa2_cache_attn_workspace_size(B, Hq, k_cache.shape[1], Lq, D, q.device.index or 0)
     return torch.zeros(n, dtype=torch.uint8, device=q.device)

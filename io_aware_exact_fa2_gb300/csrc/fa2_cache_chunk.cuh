@@ -1,5 +1,5 @@
 // fa2_cache_chunk.cuh -- attention of many query rows over the paged e4m3 cache
-// (fa2_cache_attn in include/fa2_cache.h): blocks of 128 rows on the 5th-generation
+// (fa2_cache_attn in include/fa2_cache.h): blocks of up to 256 rows on the 5th-generation
 // tensor cores.
 //
 // Mathematics.  As in fa2_cache_step.cuh, rows are the tokens of a sequence times the query

@@ -138,7 +138,7 @@ __device__ __forceinline__ int row_blocks(const AttnArgs &a, const Seq &s)
 // The line cut into `grid` ranges, the first `more` of them of size + 1 tiles.
 struct Range {
     int grid, size, more;
-    __device__ Range() = default;
+    Range() = default;
     __device__ Range(int total, int ranges) : grid(ranges), size(total / ranges), more(total - total / ranges * ranges) {}
     __device__ int begin(int c) const { return c * size + (c < more ? c : more); }
     // the range that tile x lies in
