@@ -7,7 +7,7 @@ ImportError if the library has not been built.
 
 A step's kernels take microseconds, so the checks are written for speed: each attribute of
 a tensor is read once, and structures are packed rather than built field by field (a call
-takes some 9 us of host time, 3 of them in the library; plainly written it took 22).
+takes 8 to 10 us of host time, 3 to 5 of them in the library; plainly written it took 22).
 """
 from __future__ import annotations
 
@@ -71,7 +71,13 @@ def _strides(t, shape, unit):
     if d != 1:
         raise ValueError("the last dimension must be contiguous")
     if 1 in shape:
-        a, b, c = (x if m != 1 else unit for x, m in zip((a, b, c), shape))
+        m, n, o, _ = shape
+        if m == 1:
+            a = unit
+        if n == 1:
+            b = unit
+        if o == 1:
+            c = unit
     return a, b, c
 
 
