@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     for (int cc = chunk0; cc < D / 16; cc += chunks) {
                         float4 v[4];
                         const float merged =
-                            merge_row<C, 4>(parts, first_cta, last_cta, row_at, [&](int k) { return place(cc * 4 + k); }, v);
+                            merge_row<C, 4, 2>(parts, first_cta, last_cta, row_at, [&](int k) { return place(cc * 4 + k); }, v);
                         if (live) {
 #pragma unroll
                             for (int k = 0; k < 4; k += 2)

@@ -33,8 +33,8 @@
 // us, 61 with one; D = 64, 8 rows: 41 with three, 43 with two).  Work is cut and merged as
 // in fa2_cache_line.cuh.
 // Measured: one token of 48 sequences of 64 to 8192 positions, 8 heads of 128, groups of 4:
-// 407 MB in 69 us, 5.9 TB/s, 88 % of the measured copy rate; of two of 125000: 514 MB in 86
-// us, 6.0 TB/s.  At D = 64 a tile holds half the bytes for the same softmax, and that bounds
+// 407 MB in 69 us, 5.9 TB/s, 88 % of the measured copy rate; of two of 125000: 514 MB in 84
+// us, 6.1 TB/s.  At D = 64 a tile holds half the bytes for the same softmax, and that bounds
 // it: 16 sequences of 6000, 8 heads, 98 MB in some 37 us.  Short calls are latency: of 14 us
 // for 34 MB (a window of 1024 in 16 sequences), 2 go to the launch, 1.5 to laying out the
 // line, 1 to q, 2 to merging parts.
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     for (int r = tid / TPR; r < (live < R ? live : R); r += 128 / TPR) {
                         float4 v[N];
                         auto column = [&](int k) { return (tid % TPR + k * TPR) * 4; };
-                        const float lse2 = merge_row<C, N>(parts, first_cta, last_cta, r, [&](int k) { return r * D + column(k); }, v);
+                        const float lse2 = merge_row<C, N, 4>(parts, first_cta, last_cta, r, [&](int k) { return r * D + column(k); }, v);
 #pragma unroll
                         for (int k = 0; k < N; ++k)
                             *reinterpret_cast<uint2 *>(o + sh_place[r].x + column(k)) =
