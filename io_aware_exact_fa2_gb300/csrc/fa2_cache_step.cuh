@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         volatile uint32_t *const sh_flags = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAGS);   // [2][4]
         volatile uint32_t *const sh_nan = reinterpret_cast<uint32_t *>(smem + C::OFF_NAN);       // [4]
         auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };            // the four softmax warps
-        constexpr int NONE = -100000;                                                 // reference of nothing
+        constexpr float NONE = -3.402823466e38f;   // reference of nothing: no finite score lies below it
         const bool owns_d = D > 64 || tid < 64;
 
         do {
@@ -392,7 +392,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 l[r] = psum[r] = 0.f;
             }
             uint32_t nan_rows[C::HALVES] = {};   // rows whose O at this d a visible NaN value makes NaN
-            int M = NONE;                        // (threads below R: the row's reference)
+            // The row's reference (threads below R): a float, for scores may be any; a difference of two
+            // is whole, or far past what a factor can be.
+            float M = NONE;
 
             // O^T of the tile before `g` into the registers, in the row's new frame
             auto add_tile = [&](uint32_t g) {
@@ -479,11 +481,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // the tile's references, above the maxima; a row's frame is moved by its own thread
                 auto reference = [&](int r) {
                     const float4 m4 = *reinterpret_cast<const float4 *>(sh_max + (par * R + r) * 4);
-                    return fmaxf(ceilf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))), static_cast<float>(NONE));
+                    return fmaxf(ceilf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))), NONE);
                 };
                 if (tid < R && tid < live) {
-                    const int mt = static_cast<int>(reference(tid)), now = mt > M ? mt : M;
-                    sh_frame[par * R + tid] = make_float2(pow2i(M - now), pow2i(mt - now));
+                    auto factor = [](float down) { return pow2i(static_cast<int>(fmaxf(down, -200.f))); };   // (0 from -150)
+                    const float mt = reference(tid), now = fmaxf(mt, M);
+                    sh_frame[par * R + tid] = make_float2(factor(M - now), factor(mt - now));
                     M = now;
                 }
                 // weights
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 const float4 l4 = *reinterpret_cast<const float4 *>(sh_l + tid * 4);
                 const float sum = tid < live ? (l4.x + l4.y) + (l4.z + l4.w) : 0.f;
                 sh_inv[tid] = sum == 0.f ? make_float2(0.f, -INFINITY)
-                                         : make_float2(__fdividef(1.f, sum), static_cast<float>(M) - 8.f + lg2_approx(sum));
+                                         : make_float2(__fdividef(1.f, sum), M - 8.f + lg2_approx(sum));
             }
             uint16_t *const o = static_cast<uint16_t *>(a.o);
             auto write_lse = [&](int r, float v) {
