@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             const int last_cta = cut ? sh.range.owner(line.at + line.span.tiles - 1) : cta;
             const bool alone = first_cta == last_cta;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const float lse2 = l == 0.f ? -INFINITY : M - 6.f + lg2_approx(l);
+            const float2 lse2 = l == 0.f ? make_float2(-INFINITY, 0.f) : two_floats(M, lg2_approx(l) - 6.f);
             uint16_t *const o = static_cast<uint16_t *>(a.o) + line.b * a.o_sb + hq * a.o_sh + tok * a.o_sl;
             float *const part =
                 cut ? parts.data + (2 * static_cast<size_t>(cta) + (cta == first_cta ? 1 : 0)) * Parts::slot_floats(R, D) : nullptr;
@@ -859,10 +859,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             };
             if (alone) {
                 if (chunk0 == 0 && live)
-                    write_lse(lse2);
+                    write_lse(lse2.x);
             } else {
                 if (chunk0 == 0)
-                    part[R * D + row_at] = lse2;
+                    reinterpret_cast<float2 *>(part + R * D)[row_at] = lse2;
                 // the CTA whose part is the last to arrive merges them, each row tile by itself
                 // (twins together)
                 auto sync = [&] {

@@ -32,11 +32,12 @@ constexpr int CHUNK = 16;                 // keys of the smallest piece; divides
 constexpr long long kStepRows = 16;
 
 // Parts of cut units: for each CTA two slots (its range's first unit, its last one) of
-// R rows: O fp32, R D of them in the kernel's own order, then the log2-sum-exp2 [R].
+// R rows: O fp32, R D of them in the kernel's own order, then the log2-sum-exp2 [R], each as
+// two floats (two_floats).
 struct Parts {
     int *counters;      // [grid][2]: of the units that begin in a range and go on, arrived parts
     float *data;
-    __host__ __device__ static constexpr size_t slot_floats(int R, int D) { return static_cast<size_t>(R) * (D + 1); }
+    __host__ __device__ static constexpr size_t slot_floats(int R, int D) { return static_cast<size_t>(R) * (D + 2); }
     // (the same for every configuration: calls of different ones may take the same workspace
     // in turn, and none's data may lie where another's counters do)
     static constexpr int MAX_CTAS = 4;   // an SM
@@ -281,6 +282,15 @@ __device__ __forceinline__ bool find_range(const AttnArgs &a, bool cut, LineShar
     return line.at < end;
 }
 
+// m + t as two floats that hold more of it than one.  A part counts by a power of its
+// log2-sum-exp2, so where scores are large, 10^5 say, the last place of one float, 2^-7, would
+// be half a percent of its weight.
+__device__ __forceinline__ float2 two_floats(float m, float t)
+{
+    const float sum = m + t;
+    return make_float2(sum, t - (sum - m));
+}
+
 // Merges what ranges c0 .. c1 computed of N quadruples of one row of a unit, always in that
 // order: place(k) is quadruple k's offset in a slot.  Returns the row's log2-sum-exp2.  (One
 // pass, W parts at a time: the loads of a thread's quadruples are under way together, where
@@ -298,13 +308,13 @@ __device__ __forceinline__ float merge_row(const Parts &parts, int c0, int c1, i
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int c = c0; c <= c1; c += W) {
-        float lse[W];
+        float2 lse[W];
         float4 x[W][N];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const bool there = c + i <= c1;
             const float *const s = slot(c + i);
-            lse[i] = there ? __ldcg(s + C::R * C::D + row) : -INFINITY;
+            lse[i] = there ? __ldcg(reinterpret_cast<const float2 *>(s + C::R * C::D) + row) : make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int k = 0; k < N; ++k)
                 x[i][k] = there ? __ldcg(reinterpret_cast<const float4 *>(s + place(k))) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -312,7 +322,7 @@ __device__ __forceinline__ float merge_row(const Parts &parts, int c0, int c1, i
         const float before = top;
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            top = fmaxf(top, lse[i]);
+            top = fmaxf(top, lse[i].x);
         const float ref = top == -INFINITY ? 0.f : top, f = ptx::ex2_approx(before - ref);
         l *= f;
 #pragma unroll
@@ -320,7 +330,7 @@ __device__ __forceinline__ float merge_row(const Parts &parts, int c0, int c1, i
             v[k].x *= f, v[k].y *= f, v[k].z *= f, v[k].w *= f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            const float g = ptx::ex2_approx(lse[i] - ref);
+            const float g = ptx::ex2_approx(lse[i].x - ref + lse[i].y);
             l += g;
 #pragma unroll
             for (int k = 0; k < N; ++k)

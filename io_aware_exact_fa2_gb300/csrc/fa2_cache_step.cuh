@@ -71,7 +71,7 @@ struct StepCfg {
     // factor, first and last visible key
     static constexpr int OFF_MAX = OFF_ROWS, OFF_FRAME = OFF_MAX + 2 * R * 16, OFF_SCALE = OFF_FRAME + 2 * R * 8;
     static constexpr int OFF_LO = OFF_SCALE + R * 4, OFF_HI = OFF_LO + R * 4, OFF_L = OFF_HI + R * 4;   // (OFF_L: four sums)
-    static constexpr int OFF_INV = OFF_L + R * 16, OFF_PLACE = OFF_INV + R * 8;   // 1 / sum and log2 of it; places in o and lse
+    static constexpr int OFF_INV = OFF_L + R * 16, OFF_PLACE = OFF_INV + R * 4;   // 1 / sum; places in o and lse
     static constexpr int OFF_FLAGS = OFF_PLACE + R * 16, OFF_NAN = OFF_FLAGS + 32, OFF_INFO = OFF_NAN + 16;
     static constexpr int INFO_BYTES = TILE / CHUNK * 4, OFF_BAR = OFF_INFO + 4 * INFO_BYTES;   // (ring of four tiles)
     static constexpr int NUM_BAR = 2 * SLOTS + 7;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         float *const sh_scale = reinterpret_cast<float *>(smem + C::OFF_SCALE);       // [R]
         int *const sh_lo = reinterpret_cast<int *>(smem + C::OFF_LO), *const sh_hi = reinterpret_cast<int *>(smem + C::OFF_HI);
         float *const sh_l = reinterpret_cast<float *>(smem + C::OFF_L);               // [R][4]
-        float2 *const sh_inv = reinterpret_cast<float2 *>(smem + C::OFF_INV);         // [R]
+        float *const sh_inv = reinterpret_cast<float *>(smem + C::OFF_INV);           // [R]
         longlong2 *const sh_place = reinterpret_cast<longlong2 *>(smem + C::OFF_PLACE);   // [R]; -1: not a row
         volatile uint32_t *const sh_flags = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAGS);   // [2][4]
         volatile uint32_t *const sh_nan = reinterpret_cast<uint32_t *>(smem + C::OFF_NAN);       // [4]
@@ -599,11 +599,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     sh_l[(r0 + lane) * 4 + warp] = mine;
             }
             sync();
+            float2 lse2 = make_float2(-INFINITY, 0.f);   // (threads below R)
             if (tid < R) {
                 const float4 l4 = *reinterpret_cast<const float4 *>(sh_l + tid * 4);
                 const float sum = tid < live ? (l4.x + l4.y) + (l4.z + l4.w) : 0.f;
-                sh_inv[tid] = sum == 0.f ? make_float2(0.f, -INFINITY)
-                                         : make_float2(__fdividef(1.f, sum), M - 8.f + lg2_approx(sum));
+                sh_inv[tid] = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+                if (sum != 0.f)
+                    lse2 = two_floats(M, lg2_approx(sum) - 8.f);
             }
             uint16_t *const o = static_cast<uint16_t *>(a.o);
             auto write_lse = [&](int r, float v) {
@@ -613,9 +615,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             sync();
             if (tid < R) {
                 if (alone)
-                    write_lse(tid, sh_inv[tid].y);
+                    write_lse(tid, lse2.x);
                 else
-                    part[R * D + tid] = sh_inv[tid].y;
+                    reinterpret_cast<float2 *>(part + R * D)[tid] = lse2;
             }
 #pragma unroll
             for (int r0 = 0; r0 < R; r0 += 4) {
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     const int r = r0 + k;
                     if (r >= live || !owns_d)
                         break;
-                    const float inv = sh_inv[r].x;
+                    const float inv = sh_inv[r];
 #pragma unroll
                     for (int half = 0; half < C::HALVES; ++half) {
                         const float v = nan_rows[half] >> r & 1 ? __uint_as_float(0x7fc00000u) : acc[half][r] * inv;
@@ -655,13 +657,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     for (int r = tid / TPR; r < (live < R ? live : R); r += 128 / TPR) {
                         float4 v[N];
                         auto column = [&](int k) { return (tid % TPR + k * TPR) * 4; };
-                        const float lse2 = merge_row<C, N, 4>(parts, first_cta, last_cta, r, [&](int k) { return r * D + column(k); }, v);
+                        const float merged = merge_row<C, N, 4>(parts, first_cta, last_cta, r, [&](int k) { return r * D + column(k); }, v);
 #pragma unroll
                         for (int k = 0; k < N; ++k)
                             *reinterpret_cast<uint2 *>(o + sh_place[r].x + column(k)) =
                                 make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
                         if (tid % TPR == 0)
-                            write_lse(r, lse2);
+                            write_lse(r, merged);
                     }
                 }
             }

@@ -42,23 +42,23 @@ def level_cache(D, lens, seed):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("G,Lq", ROWS)
-def test_every_score_far_below_zero(D, G, Lq):
-    """q 96, k -96: one score, -9216 sqrt(D), for every key."""
-    lens = [300, 90]
+@pytest.mark.parametrize("lens,workspace", [([300, 90], False), ([1500, 700], True)])
+def test_every_score_far_below_zero(D, G, Lq, lens, workspace):
+    """q 96, k -96: one score, -9216 sqrt(D), for every key; in one piece, and in parts that are merged."""
     c = level_cache(D, lens, D + G)
     c.k[:] = 0xfc                    # -384
     c.ks[:] = 125                    # 2^-2
     q = torch.full((2, G, Lq, D), 96.0, dtype=torch.bfloat16)
-    hold(c, G, Lq, lens, q, workspace=False)
+    hold(c, G, Lq, lens, q, workspace=workspace)
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("G,Lq", ROWS)
 @pytest.mark.parametrize("log2q,key_byte", [(6, 125), (20, 133), (60, 159)])   # k = 2^6, 2^14, 2^40
 @pytest.mark.parametrize("sign", [1, -1])
-def test_two_levels_of_large_scores(D, G, Lq, log2q, key_byte, sign):
+@pytest.mark.parametrize("lens,workspace", [([300, 90], False), ([1500, 700], True)])
+def test_two_levels_of_large_scores(D, G, Lq, log2q, key_byte, sign, lens, workspace):
     """Pages whose scores are L beside pages at 2 L: the greater take all the weight, wherever they lie."""
-    lens = [300, 90]
     c = level_cache(D, lens, D + G + log2q)
     c.k[:] = 0x78                    # 256
     c.ks[:] = key_byte
@@ -67,4 +67,4 @@ def test_two_levels_of_large_scores(D, G, Lq, log2q, key_byte, sign):
     c.ks[c.table[1, 4:6]] += 1
     c.ks[c.table[0, 17]] += 1
     q = torch.full((2, G, Lq, D), sign * 2.0 ** log2q, dtype=torch.bfloat16)
-    hold(c, G, Lq, lens, q, workspace=False)
+    hold(c, G, Lq, lens, q, workspace=workspace)
