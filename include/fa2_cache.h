@@ -172,6 +172,9 @@ fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq, int D, in
  * kernel winds down.  Outputs of that call are then undefined, and a workspace it used
  * must be zero-filled again.
  *
+ * For tests only (read on every call): FA2_TEST_STALL=2 makes some warps of fa2_cache_attn
+ * late after they have exchanged numbers, which must not change a result.
+ *
  *   detail   optional: the raw code (0 = none), the waiting role in bits 8-11, the
  *            barrier in the low byte.  Roles, up to 16 rows: 12 softmax, 13 loading,
  *            14 MMA issuer, 15 a CTA's final wait for its own work; more rows: 8, 11,

@@ -32,6 +32,10 @@ struct MoveArgs {                   // fa2_cache_write, fa2_cache_read
     int L, D;
 };
 
+// Tests only (FA2_TEST_STALL=2, read on every call): where two warps have met to exchange numbers,
+// the second of the last row tile's goes on some 20 us later.
+constexpr int TEST_LAG = 2;
+
 struct AttnArgs {
     View c;
     const void *q;
@@ -48,6 +52,7 @@ struct AttnArgs {
     int num_sms;
     int *err;                       // device error word
     unsigned long long wait_limit_ns;
+    int test;                       // TEST_LAG or 0
     cudaStream_t stream;
 };
 

@@ -3,6 +3,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdlib>
+#include <cstring>
 #include <mutex>
 
 #include "fa2_cache_step.cuh"
@@ -122,6 +123,12 @@ unsigned long long wait_limit_ns()
         return static_cast<unsigned long long>(ms > 0 ? ms : 1000) * 1000000ull;
     }();
     return limit;
+}
+
+int test_mode()
+{
+    const char *s = std::getenv("FA2_TEST_STALL");
+    return s && std::strcmp(s, "2") == 0 ? TEST_LAG : 0;
 }
 
 // (batch, head, row) element strides of a bf16 [B, H, L, D] view; NULL: contiguous.
@@ -289,6 +296,7 @@ FA2_EXPORT fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o,
     a.num_sms = fa2::cache::sm_count(dev.id());
     a.err = fa2::cache::device_error_ptr(dev.id());
     a.wait_limit_ns = fa2::cache::wait_limit_ns();
+    a.test = fa2::cache::test_mode();
     if (a.num_sms <= 0 || !a.err)
         return FA2_ERR_CUDA;
     return c->D == 64 ? fa2::cache::launch_attn_d64(a)

@@ -524,7 +524,12 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         auto all_sync = [] { asm volatile("bar.sync 11, %0;" ::"n"(256 * C::NQ) : "memory"); };
         // the two warps of the same rows
         const int pair_id = 3 + rt * 4 + (warp & 3);
-        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory"); };
+        auto pair_sync = [&] {
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory");
+            if (a.test == TEST_LAG && warp >= C::WARP_CONVERT - 4)
+                for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;)
+                    ;
+        };
         auto pair_any = [&](bool x) -> bool {
             uint32_t r;
             asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
@@ -589,6 +594,10 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 // a row with an infinity or NaN has no finite scores: make it NaN
                 const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-e);
                 const bool loads_q = !twin || rt == 0;
+                // (both have read before either writes the next number there: the scores wait
+                // for the warps that store q, but not for a twin's second)
+                if (!loads_q)
+                    pair_sync();
                 if (loads_q && loads > 0)
                     wait(C::BAR_Q_EMPTY + rt, (loads - 1) & 1);
                 if (loads_q) {

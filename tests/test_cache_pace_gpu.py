@@ -1,0 +1,29 @@
+"""Results of attention over the 8-bit cache must not depend on the pace of its warps: with the
+library's test switch FA2_TEST_STALL=2 the second of the two warps that exchange a row's numbers
+goes on some 20 us after each meeting (in the last row tile of a block), while the first runs
+ahead as far as it may."""
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+from test_cache_gpu import Cache, attend
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,Lq", [(17, 1), (2, 33), (1, 128), (4, 40)])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_a_late_warp(monkeypatch, D, G, Lq, workspace):
+    """Query rows whose halves (the two warps' shares) are of very different size, so that a number
+    exchanged at the wrong time shows; units of one row tile twice, of two, and of one alone."""
+    lens = [Lq, 700, Lq + 140]
+    c = Cache(3, 2, D, 32, lens, seed=D + G + Lq)
+    q = c.rng.standard_normal((3, 2 * G, Lq, D)) * 0.7
+    q[..., :D // 2] *= 2.0 ** -6
+    q = ref.bf16(q)
+    o, lse = attend(c, G, Lq, lens, q=q, workspace=workspace)
+    monkeypatch.setenv("FA2_TEST_STALL", "2")
+    late, late_lse = attend(c, G, Lq, lens, q=q, workspace=workspace)
+    assert torch.equal(o, late) and torch.equal(lse, late_lse)
