@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         bool more = false;
         if (lane == 0)
             more = sh.line[warp].next(a) && sh.line[warp].at < sh.end;
+        __syncwarp();                    // (a shuffle orders no memory)
         return __shfl_sync(0xffffffffu, more, 0);
     };
     // what the loading warp says of tile g: a group's scales, and whether every row sees every key

@@ -27,3 +27,16 @@ def test_a_late_warp(monkeypatch, D, G, Lq, workspace):
     monkeypatch.setenv("FA2_TEST_STALL", "2")
     late, late_lse = attend(c, G, Lq, lens, q=q, workspace=workspace)
     assert torch.equal(o, late) and torch.equal(lse, late_lse)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,Lq", [(20, 1), (2, 70)])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_from_unit_to_unit(D, G, Lq, workspace):
+    """More blocks of rows than CTAs: every warp takes its next block's sequence, head and tiles from its
+    first lane, for blocks of one tile and of several, of few rows and of many, in turn."""
+    B, H = 50, 4
+    rng = np.random.default_rng(D + Lq)
+    lens = rng.integers(1, 400, B)
+    c = Cache(B, H, D, 16, lens, seed=D + G)
+    attend(c, G, Lq, lens, rng.integers(0, Lq + 1, B), workspace=workspace)
