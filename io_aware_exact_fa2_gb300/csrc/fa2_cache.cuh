@@ -32,8 +32,8 @@ struct MoveArgs {                   // fa2_cache_write, fa2_cache_read
     int L, D;
 };
 
-// Tests only (FA2_TEST_STALL=2, read on every call): where two warps have met to exchange numbers,
-// the second of the last row tile's goes on some 20 us later.
+// Tests only (FA2_TEST_STALL=2, read on every call): where two warps of the many-row kernel have met
+// to exchange a row's largest |q|, the second of the last row tile's goes on some 20 us later.
 constexpr int TEST_LAG = 2;
 
 struct AttnArgs {

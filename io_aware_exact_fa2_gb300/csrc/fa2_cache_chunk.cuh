@@ -525,12 +525,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         auto all_sync = [] { asm volatile("bar.sync 11, %0;" ::"n"(256 * C::NQ) : "memory"); };
         // the two warps of the same rows
         const int pair_id = 3 + rt * 4 + (warp & 3);
-        auto pair_sync = [&] {
-            asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory");
-            if (a.test == TEST_LAG && warp >= C::WARP_CONVERT - 4)
-                for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;)
-                    ;
-        };
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_id) : "memory"); };
         auto pair_any = [&](bool x) -> bool {
             uint32_t r;
             asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
@@ -588,6 +583,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 }
                 pair[tid] = __uint_as_float(top);
                 pair_sync();
+                if (a.test == TEST_LAG && warp >= C::WARP_CONVERT - 4)
+                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;)
+                        ;
                 top = max(top, __float_as_uint(pair[tid ^ 128]));
                 // 448 = 1.75 * 2^8
                 e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) >= 0x60u ? 1 : 0);

@@ -1,6 +1,6 @@
 """Results of attention over the 8-bit cache must not depend on the pace of its warps: with the
-library's test switch FA2_TEST_STALL=2 the second of the two warps that exchange a row's numbers
-goes on some 20 us after each meeting (in the last row tile of a block), while the first runs
+library's test switch FA2_TEST_STALL=2 the second of the two warps that exchange a row's largest
+|q| reads its partner's some 20 us late (in the last row tile of a block), while the first runs
 ahead as far as it may."""
 import numpy as np
 import pytest
