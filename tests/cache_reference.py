@@ -163,3 +163,24 @@ def check_attention(o, lse, ref, fill=None):
 
 def bf16(x):
     return torch.from_numpy(np.ascontiguousarray(x)).to(torch.bfloat16)
+
+
+def check_beside_nan(o, lse, q, kc, vc, ks, vs, table, kv_lens, q_lens, causal, window, scale):
+    """As check_attention, where values hold NaN: a column of O is no other column's, so those that
+    no NaN reaches are held to the answer, and its bound, of the cache with numbers in their places
+    (attention()'s own bound takes the largest value of all columns and is NaN there)."""
+    rest = (q, kc, vc, ks, vs, table, kv_lens, q_lens, causal, window, scale)
+    ro, rl, _, _ = attention(*rest)
+    clean = (q, kc, np.where((vc & 0x7f) == 0x7f, 0, vc), ks, np.where(vs == 255, 127, vs), *rest[5:])
+    co, cl, bo, bl = attention(*clean)
+    o, lse = o.double().numpy(), lse.double().numpy()
+    written = ~np.isnan(bl) | np.isnan(cl)
+    for got, nan_of, want, bound, name in ((lse, rl, cl, bl, "lse"), (o, ro, co, bo, "o")):
+        live = written if got.ndim == 3 else np.broadcast_to(written[..., None], got.shape)
+        nan = np.isnan(nan_of) & live
+        assert np.array_equal(np.isnan(got) & live, nan), f"{name}: NaN in other places"
+        ok = live & ~nan & ~np.isinf(want)
+        assert np.isfinite(bound[ok]).all() and np.array_equal(got[live & np.isinf(want)], want[live & np.isinf(want)]), name
+        over = np.abs(got[ok] - want[ok]) - bound[ok]
+        assert not over.size or over.max() <= 0, \
+            f"{name}: {over.max():.3e} over its bound, at {np.argwhere(ok)[over.argmax()]}"
