@@ -124,11 +124,16 @@ fa2_status fa2_cache_read(const fa2_cache *c, void *k, void *v, const long long 
  * as they are, with q as a sum of two e4m3 numbers times a power of two of its row:
  * that is q itself but for elements far below their row's largest, which are off by
  * at most 2^-21 of it (up to 16 rows, Lq * Hq / H) or 2^-17 (more).  Sums and softmax
- * are fp32; softmax weights are rounded to three e4m3 terms (12 bits; up to 16 rows)
- * or to fp16 (11 bits) for the product with V.  A row of q with an infinity or NaN
- * gives NaN.  Scales are those that fa2_cache_write gives, 2^-96 to 2^119, or NaN;
- * keys whose value scale is more than 2^100 below the largest that a row sees may be
- * missing from its sums (a page of zeros has 2^-96).
+ * are fp32; for the product with V a softmax weight is rounded to fp16 (11 bits), and up
+ * to 16 rows taken as three e4m3 terms, which hold that.  What is rounded is the weight
+ * times its page's value scale, against the largest such product, so a small one is off by
+ * an absolute amount: 2^-25 of the largest among the 128 keys of its tile (up to 16 rows),
+ * 2^-31 of the largest that the row sees (more rows).  A column of O in which strong pages
+ * hold zeros shows it: values of pages weaker by more than that are lost there.  The sum of
+ * the weights, and with it LSE, has no part in this; from it, keys may be missing whose
+ * value scale is more than 2^100 below the largest that the row sees (a page of zeros has
+ * 2^-96).  A row of q with an infinity or NaN gives NaN.  Scales are those that
+ * fa2_cache_write gives, 2^-96 to 2^119, or NaN.
  *
  *   q          bf16 [B, Hq, Lq, D] device view, strides (batch, head, row) or NULL.
  *   o          bf16 [B, Hq, Lq, D] device view (written), likewise; its rows must not overlap

@@ -68,3 +68,47 @@ def test_two_levels_of_large_scores(D, G, Lq, log2q, key_byte, sign, lens, works
     c.ks[c.table[0, 17]] += 1
     q = torch.full((2, G, Lq, D), sign * 2.0 ** log2q, dtype=torch.bfloat16)
     hold(c, G, Lq, lens, q, workspace=workspace)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 16, 20, 200])
+@pytest.mark.parametrize("apart", [12, 24, 30, 35, 40])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_value_scales_far_apart(D, rows, apart, workspace):
+    """Some pages' values are 2^apart stronger, but zero in half of the columns, where O is the weaker
+    ones' alone.  A weight times its value scale is off by 2^-11 of itself, and by a part of the
+    largest such product: 2^-25 of the largest in its tile of 128 keys (up to 16 rows; half a step of
+    the last term, 2^-9 / 256 / 2, of weights that end between 2^7 and 2^8), 2^-31 of the row's (more;
+    half a step of a small fp16, 2^-25, of weights that end at 2^6 or above)."""
+    n, G = 700, rows
+    c = Cache(1, 1, D, 16, [n], seed=D + rows + apart, nan_after=False)
+    strong = c.table[0, [1, 9, 10, 30]]
+    c.v[strong, :, :, ::2] = 0
+    c.vs[:] = 110
+    c.vs[strong] = 110 + apart
+    q = ref.bf16(c.rng.standard_normal((1, G, 1, D)) * 0.5)
+    o, lse = attend(c, G, 1, [n], q=q, workspace=workspace, check=False)
+    args = (c.ks, c.vs, c.table, [n], None, True, None, D ** -0.5)
+    qn = q.double().numpy()
+    want, want_lse, _, lse_bound = ref.attention(qn, c.k, c.v, *args)
+    assert (np.abs(lse.double().cpu().numpy() - want_lse) <= lse_bound).all()
+    mass = ref.attention(qn, c.k, c.v & 0x7f, *args)[0]
+    k, _ = ref.gather(c.k, c.ks, c.table[0], 0, n)
+    codes, _ = ref.gather(c.v & 0x7f, np.full_like(c.vs, 127), c.table[0], 0, n)
+    scale = np.repeat(ref.scale_value(c.vs[c.table[0], 0]), 16)[:n]
+    tile = np.arange(n) // 128
+    for r in range(rows):
+        s = k @ qn[0, r, 0] * D ** -0.5
+        w = np.exp(s - want_lse[0, r, 0])
+        # scores' error, as cache_reference.attention derives it
+        ds = (np.abs(k) @ np.abs(qn[0, r, 0])).max() * D ** -0.5 * 2 * D * 2.0 ** -23 + 2.0 ** -20 * (1 + np.abs(s).max()) + \
+            D ** -0.5 * (2.0 ** -21 if rows <= 16 else 2.0 ** -17) * np.abs(qn[0, r, 0]).max() * np.abs(k).sum(1).max()
+        if rows <= 16:
+            top = np.zeros(tile[-1] + 1)
+            np.maximum.at(top, tile, w * scale)
+            small = 2.0 ** -25 * top[tile] @ codes
+        else:
+            small = 2.0 ** -31 * (w * scale).max() * codes.sum(0)
+        bound = 2.0 ** -8 * np.abs(want[0, r, 0]) + (1 + 2.0 ** -8) * ((2.0 ** -11 + 2 * ds + n * 2.0 ** -22) * mass[0, r, 0] + small)
+        over = np.abs(o[0, r, 0].double().cpu().numpy() - want[0, r, 0]) - bound
+        assert over.max() <= 0, f"row {r}: {over.max():.3e} over its bound"
