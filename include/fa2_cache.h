@@ -77,15 +77,17 @@ typedef struct fa2_cache {
  *   starts     int32 [B] device: tokens each sequence holds already.  Rows at
  *              negative positions are dropped.
  *   counts     int32 [B] device, 0..L: rows to write; NULL: L for all.
- *   L          rows a sequence in k and v, at most 2^30 (0: no-op).
+ *   L          rows a sequence in k and v, at most 2^30 (0: no-op).  A call's blocks, one for
+ *              keys and one for values of each page that L rows can touch (write) or of each
+ *              8192 / D rows (read), of B * H heads, are at most 2^31 - 1.
  *
  * A page that gets rows must be named once among the touched entries of the
  * page table: two sequences that write into one page race, and its contents
  * are then undefined.  Reading shared pages is always fine.
  *
  * Errors: FA2_ERR_INVALID_ARG for null or misaligned pointers, sizes or strides
- * that break the rules above; FA2_ERR_UNSUPPORTED for another D or page_size;
- * FA2_ERR_CUDA.
+ * that break the rules above; FA2_ERR_UNSUPPORTED for another D or page_size, or more
+ * blocks than that; FA2_ERR_CUDA.
  */
 fa2_status fa2_cache_write(const fa2_cache *c, const void *k, const void *v, const long long *k_strides,
                            const long long *v_strides, const int *starts, const int *counts, int L,

@@ -56,6 +56,9 @@ struct AttnArgs {
     cudaStream_t stream;
 };
 
+// Blocks of a write or read, which a launch counts in an int.
+long long write_blocks(const MoveArgs &a);
+long long read_blocks(const MoveArgs &a);
 fa2_status launch_write(const MoveArgs &a, cudaStream_t stream);
 fa2_status launch_read(const MoveArgs &a, cudaStream_t stream);
 fa2_status launch_attn_d64(const AttnArgs &a);

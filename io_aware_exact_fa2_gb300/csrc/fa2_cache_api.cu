@@ -219,6 +219,8 @@ fa2_status move(const fa2_cache *c, void *k, void *v, const long long *k_strides
     a.counts = counts;
     a.L = L;
     a.D = c->D;
+    if ((write ? write_blocks(a) : read_blocks(a)) > INT_MAX)
+        return FA2_ERR_UNSUPPORTED;
     const Device dev(c->k);
     if (dev.status() != FA2_OK)
         return dev.status();

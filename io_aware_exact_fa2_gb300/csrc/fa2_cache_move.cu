@@ -260,17 +260,34 @@ __global__ void __launch_bounds__(READ_T) read_kernel(const MoveArgs a, const in
     }
 }
 
+// Threads a row, 16 values each, as a power of two.
+int row_shift(int D) { return D == 64 ? 2 : D == 128 ? 3 : 4; }
+
+// Pages that L rows can touch: one, and one more for every page_size rows after the first.
+int touched_pages(const MoveArgs &a)
+{
+    const int page_size = 1 << a.c.page_shift;
+    return static_cast<int>((static_cast<long long>(a.L) + page_size - 2) / page_size) + 1;
+}
+
+// Blocks that read L rows of a head.
+int read_chunks(const MoveArgs &a)
+{
+    const int rows = (READ_T >> row_shift(a.D)) * READ_ROWS;
+    return static_cast<int>((static_cast<long long>(a.L) + rows - 1) / rows);
+}
+
 }  // namespace
+
+// (B H and what they are multiplied by are below 2^31 each)
+long long write_blocks(const MoveArgs &a) { return 2 * (static_cast<long long>(a.c.B) * a.c.H * touched_pages(a)); }
+long long read_blocks(const MoveArgs &a) { return 2 * (static_cast<long long>(a.c.B) * a.c.H * read_chunks(a)); }
 
 fa2_status launch_write(const MoveArgs &a, cudaStream_t stream)
 {
     const int page_size = 1 << a.c.page_shift;
-    const int lpr_shift = a.D == 64 ? 2 : a.D == 128 ? 3 : 4;
-    // pages that L rows can touch: one, and one more for every page_size rows after the first
-    const int touched = static_cast<int>((static_cast<long long>(a.L) + page_size - 2) / page_size) + 1;
-    const long long blocks = 2ll * a.c.B * a.c.H * touched;
-    if (blocks > INT_MAX)
-        return FA2_ERR_INVALID_ARG;
+    const int lpr_shift = row_shift(a.D), touched = touched_pages(a);
+    const long long blocks = write_blocks(a);
     // A page's rows in pieces of 16 values, four a thread where there are enough: in flight
     // together they hide each other's latency, and short blocks the next one's.  (Half a
     // million rows of 64, 134 MB: pages of 64 41 us with one piece, 29 with four, 31 with
@@ -293,13 +310,7 @@ fa2_status launch_write(const MoveArgs &a, cudaStream_t stream)
 
 fa2_status launch_read(const MoveArgs &a, cudaStream_t stream)
 {
-    const int lpr_shift = a.D == 64 ? 2 : a.D == 128 ? 3 : 4;
-    const int rows = (READ_T >> lpr_shift) * READ_ROWS;
-    const int chunks = static_cast<int>((static_cast<long long>(a.L) + rows - 1) / rows);
-    const long long blocks = 2ll * a.c.B * a.c.H * chunks;
-    if (blocks > INT_MAX)
-        return FA2_ERR_INVALID_ARG;
-    read_kernel<<<static_cast<unsigned>(blocks), READ_T, 0, stream>>>(a, chunks, lpr_shift);
+    read_kernel<<<static_cast<unsigned>(read_blocks(a)), READ_T, 0, stream>>>(a, read_chunks(a), row_shift(a.D));
     return cudaGetLastError() == cudaSuccess ? FA2_OK : FA2_ERR_CUDA;
 }
 
