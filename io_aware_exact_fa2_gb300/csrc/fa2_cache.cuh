@@ -32,8 +32,9 @@ struct MoveArgs {                   // fa2_cache_write, fa2_cache_read
     int L, D;
 };
 
-// Tests only (FA2_TEST_STALL=2, read on every call): where two warps of the many-row kernel have met
-// to exchange a row's largest |q|, the second of the last row tile's goes on some 20 us later.
+// Tests only (FA2_TEST_STALL=2, read on every call): some 20 us late are the few-row kernel's loading
+// warp, and, where two warps of the many-row kernel have met to exchange a row's largest |q|, the
+// second of the last row tile's.
 constexpr int TEST_LAG = 2;
 
 struct AttnArgs {
@@ -51,7 +52,7 @@ struct AttnArgs {
     size_t workspace_bytes;
     int num_sms;
     int *err;                       // device error word
-    unsigned long long wait_limit_ns;
+    unsigned long long wait_limit_ns, drain_limit_ns;   // of waits between warps; for a CTA's own copies and products
     int test;                       // TEST_LAG or 0
     cudaStream_t stream;
 };

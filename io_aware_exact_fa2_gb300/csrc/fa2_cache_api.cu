@@ -131,6 +131,15 @@ int test_mode()
     return s && std::strcmp(s, "2") == 0 ? TEST_LAG : 0;
 }
 
+// The limit of a call's waits between warps: FA2_TEST_WAIT_LIMIT_NS (read on every call) makes it so
+// short that they run out, for tests.
+unsigned long long call_wait_limit_ns()
+{
+    const char *s = std::getenv("FA2_TEST_WAIT_LIMIT_NS");
+    const long long ns = s ? std::atoll(s) : 0;
+    return ns > 0 ? static_cast<unsigned long long>(ns) : wait_limit_ns();
+}
+
 // (batch, head, row) element strides of a bf16 [B, H, L, D] view; NULL: contiguous.
 bool row_strides(const long long *given, int H, int L, int D, long long &b, long long &h, long long &l)
 {
@@ -297,8 +306,9 @@ FA2_EXPORT fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o,
         return dev.status();
     a.num_sms = fa2::cache::sm_count(dev.id());
     a.err = fa2::cache::device_error_ptr(dev.id());
-    a.wait_limit_ns = fa2::cache::wait_limit_ns();
     a.test = fa2::cache::test_mode();
+    a.drain_limit_ns = fa2::cache::wait_limit_ns();
+    a.wait_limit_ns = fa2::cache::call_wait_limit_ns();
     if (a.num_sms <= 0 || !a.err)
         return FA2_ERR_CUDA;
     return c->D == 64 ? fa2::cache::launch_attn_d64(a)

@@ -191,6 +191,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
     auto warp_wait = [&](int i, uint32_t parity, int code) -> bool {
         return wait_phase(bar(i), parity, a.err, code | i, limit);
     };
+    auto drain_wait = [&](int i, uint32_t parity) {
+        wait_phase(bar(i), parity, a.err, CHUNK_ERR_DRAIN | i, a.drain_limit_ns);
+    };
     auto warp_arrive = [&](int i) {
         __syncwarp();
         if (lane == 0)
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 } while (more);
                 // nothing issued is still running when tensor memory is given back
                 mma_commit(bar(C::BAR_DRAIN));
-                lone_wait(bar(C::BAR_DRAIN), 0, a.err, CHUNK_ERR_DRAIN | C::BAR_DRAIN, limit);
+                lone_wait(bar(C::BAR_DRAIN), 0, a.err, CHUNK_ERR_DRAIN | C::BAR_DRAIN, a.drain_limit_ns);
             }
             __syncwarp();
         } else if (warp == C::WARP_LOAD) {
@@ -432,9 +435,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             } while (ok && next_unit());
             // the copies in flight have landed before the CTA goes
             for (uint32_t g = issued > C::VS ? issued - C::VS : 0; g < issued; ++g) {
-                warp_wait(C::BAR_RAW_FULL + g % C::VS, g / C::VS & 1, CHUNK_ERR_DRAIN);
+                drain_wait(C::BAR_RAW_FULL + g % C::VS, g / C::VS & 1);
                 if (g + C::KS >= issued)
-                    warp_wait(C::BAR_K_FULL + g % C::KS, g / C::KS & 1, CHUNK_ERR_DRAIN);
+                    drain_wait(C::BAR_K_FULL + g % C::KS, g / C::KS & 1);
             }
         }
     } else if (warp >= C::WARP_CONVERT) {

@@ -175,6 +175,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         const uint32_t page_bytes = static_cast<uint32_t>(D) << a.c.page_shift;
         const uint32_t offset = static_cast<uint32_t>(lane) * C::ROW << a.c.page_shift;   // in each panel
         uint32_t issued = 0;                               // items
+        if (a.test == TEST_LAG)
+            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;)
+                ;
         do {
             int tile0, tile1;
             part_of(tile0, tile1);
@@ -230,8 +233,8 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         } while (ok && next_unit());
         // the copies in flight have landed before the CTA goes
         for (uint32_t item = issued > SLOTS ? issued - SLOTS : 0; item < issued; ++item) {
-            ok = true;
-            warp_wait(C::BAR_FULL + item % SLOTS, item / SLOTS & 1, STEP_ERR_DRAIN);
+            const int i = C::BAR_FULL + item % SLOTS;
+            wait_phase(bar(i), item / SLOTS & 1, a.err, STEP_ERR_DRAIN | i, a.drain_limit_ns);
         }
     } else if (warp == C::WARP_MMA) {
         // ============================================ one thread issues the products
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             } while (ok && next_unit());
             // nothing issued is still running when tensor memory is given back
             mma_commit(bar(C::BAR_DRAIN));
-            lone_wait(bar(C::BAR_DRAIN), 0, a.err, STEP_ERR_DRAIN | C::BAR_DRAIN, a.wait_limit_ns);
+            lone_wait(bar(C::BAR_DRAIN), 0, a.err, STEP_ERR_DRAIN | C::BAR_DRAIN, a.drain_limit_ns);
         }
         __syncwarp();
     } else {

@@ -1,7 +1,7 @@
 """Results of attention over the 8-bit cache must not depend on the pace of its warps: with the
 library's test switch FA2_TEST_STALL=2 the second of the two warps that exchange a row's largest
-|q| reads its partner's some 20 us late (in the last row tile of a block), while the first runs
-ahead as far as it may."""
+|q| reads its partner's some 20 us late (in the last row tile of a block of many rows), and the
+warp that loads the keys of few rows begins as late, while the others run ahead as far as they may."""
 import numpy as np
 import pytest
 import torch
@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("G,Lq", [(17, 1), (2, 33), (1, 128), (4, 40)])
+@pytest.mark.parametrize("G,Lq", [(17, 1), (2, 33), (1, 128), (4, 40), (1, 3), (16, 1)])
 @pytest.mark.parametrize("workspace", [False, True])
 def test_a_late_warp(monkeypatch, D, G, Lq, workspace):
     """Query rows whose halves (the two warps' shares) are of very different size, so that a number
