@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import cache_reference as ref
-from test_cache_gpu import Cache, attend
+from test_cache_gpu import DEV, Cache, attend, fa2, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,28 @@ def test_from_unit_to_unit(D, G, Lq, workspace):
     lens = rng.integers(1, 400, B)
     c = Cache(B, H, D, 16, lens, seed=D + G)
     attend(c, G, Lq, lens, rng.integers(0, Lq + 1, B), workspace=workspace)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,Lq", [(8, 1), (16, 1), (20, 1), (3, 100)])
+def test_every_counter_is_left_at_zero(D, G, Lq):
+    """Two contexts over all CTAs, up to three an SM: the counters of all of them (8 bytes a CTA, room for
+    four CTAs an SM, in 256-byte steps) are zero after each call, and each gives the same bits."""
+    lens = [60011, 20007]
+    c = Cache(2, 1, D, 128, lens, seed=D + G, nan_after=False)
+    dev, q = c.device(), ref.bf16(c.rng.standard_normal((2, G, Lq, D))).to(DEV)
+    kv = i32(lens)
+    sms = torch.cuda.get_device_properties(DEV).multi_processor_count
+    region = (sms * 4 * 8 + 255) // 256 * 256
+    ws = fa2().fa2_cache_attn_workspace(q, dev[0])
+    assert ws.numel() > region
+    outs = []
+    for _ in range(3):
+        o, lse = torch.zeros_like(q), torch.zeros(2, G, Lq, device=DEV)
+        fa2().fa2_cache_attn(q, *dev, kv, o, lse, workspace=ws)
+        assert not ws[:region].any()
+        outs.append((o, lse))
+    assert ws[region:].any()    # (parts were left there)
+    assert all(torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1]) for o, lse in outs)
+    assert torch.isfinite(outs[0][0]).all()
+    assert fa2().fa2_cache_get_device_error() == (0, 0)
