@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         __syncwarp();
         bool more = false;
         if (lane == 0)
-            more = sh.line[warp].next(a) && sh.line[warp].at < sh.end;
+            more = sh.line[warp].next(a, sh.end);
         __syncwarp();                    // (a shuffle orders no memory)
         return __shfl_sync(0xffffffffu, more, 0);
     };
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         loads[q] += q == 0 || !twin;
                     }
                     Line<C> &mine = sh.line[C::WARP_MMA];
-                    more = ok && mine.next(a) && mine.at < sh.end;
+                    more = ok && mine.next(a, sh.end);
                 } while (more);
                 // nothing issued is still running when tensor memory is given back
                 mma_commit(bar(C::BAR_DRAIN));

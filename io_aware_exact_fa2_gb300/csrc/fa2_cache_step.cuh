@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         tile0 = cut && first > line.at ? first - line.at : 0;
         tile1 = cut && end < line.at + line.span.tiles ? end - line.at : line.span.tiles;
     };
-    auto next_unit = [&]() { return line.next(a) && line.at < end; };
+    auto next_unit = [&]() { return line.next(a, end); };
     uint32_t *const sh_info = reinterpret_cast<uint32_t *>(smem + C::OFF_INFO);   // [4][8 groups of 16 keys]
     // tile g's keys are item 2 g of the ring, its values item 2 g + 1
     uint32_t it = 0, unit = 0;   // tiles and units before the present unit
