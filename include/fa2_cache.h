@@ -181,8 +181,8 @@ fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq, int D, in
  *
  * For tests only (read on every call): FA2_TEST_WAIT_LIMIT_NS sets the limit of the waits
  * between fa2_cache_attn's warps (not of those for a CTA's own copies and products);
- * FA2_TEST_STALL=2 makes some of the warps 20 us late, which must not change a result, but
- * with a limit of a nanosecond lets the others' waits on them run out.
+ * FA2_TEST_STALL=2 makes some of the warps tens of microseconds late, which must not change
+ * a result, but with a limit of a nanosecond lets the others' waits on them run out.
  *
  *   detail   optional: the raw code (0 = none), the waiting role in bits 8-11, the
  *            barrier in the low byte.  Roles, up to 16 rows: 12 softmax, 13 loading,

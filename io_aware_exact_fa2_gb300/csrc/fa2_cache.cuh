@@ -32,10 +32,11 @@ struct MoveArgs {                   // fa2_cache_write, fa2_cache_read
     int L, D;
 };
 
-// Tests only (FA2_TEST_STALL=2, read on every call): some 20 us late are the few-row kernel's loading
-// warp, and, where two warps of the many-row kernel have met to exchange a row's largest |q|, the
-// second of the last row tile's.
-constexpr int TEST_LAG = 2;
+// Tests only (FA2_TEST_STALL=2, read on every call): some warps take naps of about half a microsecond,
+// the few-row kernel's loading warp before it begins, and, where two warps of the many-row kernel have
+// met to exchange a row's largest |q|, the second of the last row tile's.  (A count, and no test of
+// it, in the kernels: the many-row one took 387 us instead of 384 with a branch there.)
+constexpr int TEST_NAPS = 64;
 
 struct AttnArgs {
     View c;
@@ -53,7 +54,7 @@ struct AttnArgs {
     int num_sms;
     int *err;                       // device error word
     unsigned long long wait_limit_ns, drain_limit_ns;   // of waits between warps; for a CTA's own copies and products
-    int test;                       // TEST_LAG or 0
+    int naps;                       // tests only: TEST_NAPS or 0
     cudaStream_t stream;
 };
 

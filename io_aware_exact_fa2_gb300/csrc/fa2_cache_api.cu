@@ -125,10 +125,10 @@ unsigned long long wait_limit_ns()
     return limit;
 }
 
-int test_mode()
+int test_naps()
 {
     const char *s = std::getenv("FA2_TEST_STALL");
-    return s && std::strcmp(s, "2") == 0 ? TEST_LAG : 0;
+    return s && std::strcmp(s, "2") == 0 ? TEST_NAPS : 0;
 }
 
 // The limit of a call's waits between warps: FA2_TEST_WAIT_LIMIT_NS (read on every call) makes it so
@@ -306,7 +306,7 @@ FA2_EXPORT fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o,
         return dev.status();
     a.num_sms = fa2::cache::sm_count(dev.id());
     a.err = fa2::cache::device_error_ptr(dev.id());
-    a.test = fa2::cache::test_mode();
+    a.naps = fa2::cache::test_naps();
     a.drain_limit_ns = fa2::cache::wait_limit_ns();
     a.wait_limit_ns = fa2::cache::call_wait_limit_ns();
     if (a.num_sms <= 0 || !a.err)

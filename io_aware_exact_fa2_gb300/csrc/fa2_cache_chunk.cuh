@@ -586,9 +586,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                 }
                 pair[tid] = __uint_as_float(top);
                 pair_sync();
-                if (a.test == TEST_LAG && warp >= C::WARP_CONVERT - 4)
-                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;)
-                        ;
+#pragma unroll 1
+                for (int i = warp >= C::WARP_CONVERT - 4 ? a.naps : 0; i > 0; --i)
+                    __nanosleep(500);
                 top = max(top, __float_as_uint(pair[tid ^ 128]));
                 // 448 = 1.75 * 2^8
                 e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) >= 0x60u ? 1 : 0);

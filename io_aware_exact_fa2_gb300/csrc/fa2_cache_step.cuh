@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
         const uint32_t page_bytes = static_cast<uint32_t>(D) << a.c.page_shift;
         const uint32_t offset = static_cast<uint32_t>(lane) * C::ROW << a.c.page_shift;   // in each panel
         uint32_t issued = 0;                               // items
-        if (a.test == TEST_LAG)
-            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;)
-                ;
+#pragma unroll 1
+        for (int i = a.naps; i > 0; --i)
+            __nanosleep(500);
         do {
             int tile0, tile1;
             part_of(tile0, tile1);

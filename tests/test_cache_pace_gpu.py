@@ -1,7 +1,8 @@
 """Results of attention over the 8-bit cache must not depend on the pace of its warps: with the
 library's test switch FA2_TEST_STALL=2 the second of the two warps that exchange a row's largest
-|q| reads its partner's some 20 us late (in the last row tile of a block of many rows), and the
-warp that loads the keys of few rows begins as late, while the others run ahead as far as they may."""
+|q| reads its partner's tens of microseconds late (in the last row tile of a block of many rows),
+and the warp that loads the keys of few rows begins as late, while the others run ahead as far as
+they may."""
 import numpy as np
 import pytest
 import torch

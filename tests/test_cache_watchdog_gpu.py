@@ -1,7 +1,7 @@
 """The 8-bit cache's bounded waits: one that runs out is reported by fa2_cache_get_device_error, the
 kernel winds down, writes nothing but its rows, and the next call on the context is right.
 
-The time-outs are made on purpose: FA2_TEST_STALL=2 makes some warps 20 us late, and with
+The time-outs are made on purpose: FA2_TEST_STALL=2 makes some warps tens of microseconds late, and with
 FA2_TEST_WAIT_LIMIT_NS=1 the issuing warp does not wait so long; then the waits of the softmax, loading
 and converting warps on it run out in turn.  Nothing faults: a role that has given up waiting runs on to
 its end, with addresses that do not depend on what it waited for, and the copies and products in
