@@ -12,6 +12,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "fa2_host.h"
 #include "fa2_launch.cuh"
 
 #define FA2_EXPORT extern "C" __attribute__((visibility("default")))
@@ -26,7 +27,6 @@ void *noalloc_scratch_ptr(int dev);
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr double kLog2e = 1.4426950408889634074;  // log2(e) = 1 / ln 2
 
 EncodeTiledFn encode_fn()
@@ -44,29 +44,6 @@ EncodeTiledFn encode_fn()
             (void)cudaGetLastError();
     });
     return fn;
-}
-
-unsigned long long wait_limit_ns()
-{
-    static unsigned long long limit = [] {
-        const char *s = std::getenv("FA2_WAIT_LIMIT_MS");
-        long long ms = s ? std::atoll(s) : 0;
-        if (ms <= 0)
-            ms = 1000;
-        return static_cast<unsigned long long>(ms) * 1000000ull;
-    }();
-    return limit;
-}
-
-// Limit of the forward kernel's waits between its warps.  FA2_TEST_WAIT_LIMIT_NS
-// (read on every call, nanoseconds) shortens it so that a test of the time-out path
-// ends quickly; the waits with which a CTA drains its own copies and MMAs before
-// exiting keep the full limit.
-unsigned long long fwd_wait_limit_ns()
-{
-    const char *s = std::getenv("FA2_TEST_WAIT_LIMIT_NS");
-    const long long ns = s ? std::atoll(s) : 0;
-    return ns > 0 ? static_cast<unsigned long long>(ns) : wait_limit_ns();
 }
 
 // Tests of the time-out path: FA2_TEST_STALL=1 (read on every call) makes the forward
@@ -90,24 +67,6 @@ int split_policy()
     if (s && std::strcmp(s, "never") == 0)
         return SPLIT_NEVER;
     return SPLIT_AUTO;
-}
-
-// Number of SMs of a device (looked up once per device).
-int sm_count(int dev)
-{
-    static std::mutex mu;
-    static int cache[kMaxDevices] = {};
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev >= 0 && dev < kMaxDevices && cache[dev] > 0)
-        return cache[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-        (void)cudaGetLastError();
-        return 0;
-    }
-    if (dev >= 0 && dev < kMaxDevices)
-        cache[dev] = n;
-    return n;
 }
 
 // Device address of g_device_error for the current device (looked up once per device).
@@ -234,7 +193,7 @@ fa2_status launch(const void *q, const void *k, const void *v, void *o, float *l
     a.window = window;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
     a.err = device_error_ptr(dev);
-    a.wait_limit_ns = fwd_wait_limit_ns();
+    a.wait_limit_ns = call_wait_limit_ns();
     a.drain_limit_ns = wait_limit_ns();
     a.stall_test = fwd_stall_test();
     a.stream = stream;

@@ -63,13 +63,12 @@ long long write_blocks(const MoveArgs &a);
 long long read_blocks(const MoveArgs &a);
 fa2_status launch_write(const MoveArgs &a, cudaStream_t stream);
 fa2_status launch_read(const MoveArgs &a, cudaStream_t stream);
-fa2_status launch_attn_d64(const AttnArgs &a);
-fa2_status launch_attn_d128(const AttnArgs &a);
-fa2_status launch_attn_d256(const AttnArgs &a);
+// Head dimension D, 64, 128 or 256 (fa2_cache_attn_d*.cu).
+template <int D>
+fa2_status launch_attn(const AttnArgs &a);
 // Workspace bytes for `rows` query rows a key/value head.
-size_t attn_workspace_d64(long long rows, int num_sms);
-size_t attn_workspace_d128(long long rows, int num_sms);
-size_t attn_workspace_d256(long long rows, int num_sms);
+template <int D>
+size_t attn_workspace_bytes(long long rows, int num_sms);
 
 constexpr int kMinExponent = -96;   // of a scale that fa2_cache_write sets
 constexpr int kMaxExponent = 119;   // 448 * 2^119 is the largest finite product in fp32 and bf16

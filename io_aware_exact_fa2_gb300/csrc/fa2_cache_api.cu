@@ -6,7 +6,8 @@
 #include <cstring>
 #include <mutex>
 
-#include "fa2_cache_step.cuh"
+#include "fa2_cache_tile.cuh"
+#include "fa2_host.h"
 
 #define FA2_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -33,7 +34,6 @@ EncodeTiled encode_tiled()
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr long long kMaxStride = 1ll << 38;
 constexpr long long kMaxLength = 1ll << 30;   // positions of a sequence, rows of a call
 
@@ -79,23 +79,6 @@ private:
     fa2_status status_ = FA2_ERR_CUDA;
 };
 
-int sm_count(int dev)
-{
-    static std::mutex mu;
-    static int cache[kMaxDevices] = {};
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev >= 0 && dev < kMaxDevices && cache[dev] > 0)
-        return cache[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-        (void)cudaGetLastError();
-        return 0;
-    }
-    if (dev >= 0 && dev < kMaxDevices)
-        cache[dev] = n;
-    return n;
-}
-
 // Device address of g_cache_error on `dev`, which must be current (looked up once per device).
 int *device_error_ptr(int dev)
 {
@@ -114,30 +97,10 @@ int *device_error_ptr(int dev)
     return static_cast<int *>(ptr);
 }
 
-// Limit of the kernels' waits between warps (FA2_WAIT_LIMIT_MS, read once).
-unsigned long long wait_limit_ns()
-{
-    static const unsigned long long limit = [] {
-        const char *s = std::getenv("FA2_WAIT_LIMIT_MS");
-        const long long ms = s ? std::atoll(s) : 0;
-        return static_cast<unsigned long long>(ms > 0 ? ms : 1000) * 1000000ull;
-    }();
-    return limit;
-}
-
 int test_naps()
 {
     const char *s = std::getenv("FA2_TEST_STALL");
     return s && std::strcmp(s, "2") == 0 ? TEST_NAPS : 0;
-}
-
-// The limit of a call's waits between warps: FA2_TEST_WAIT_LIMIT_NS (read on every call) makes it so
-// short that they run out, for tests.
-unsigned long long call_wait_limit_ns()
-{
-    const char *s = std::getenv("FA2_TEST_WAIT_LIMIT_NS");
-    const long long ns = s ? std::atoll(s) : 0;
-    return ns > 0 ? static_cast<unsigned long long>(ns) : wait_limit_ns();
 }
 
 // (batch, head, row) element strides of a bf16 [B, H, L, D] view; NULL: contiguous.
@@ -238,8 +201,9 @@ fa2_status move(const fa2_cache *c, void *k, void *v, const long long *k_strides
 
 size_t workspace_bytes(int D, long long rows, int num_sms)
 {
-    return D == 64 ? attn_workspace_d64(rows, num_sms)
-                   : D == 128 ? attn_workspace_d128(rows, num_sms) : attn_workspace_d256(rows, num_sms);
+    return D == 64    ? attn_workspace_bytes<64>(rows, num_sms)
+           : D == 128 ? attn_workspace_bytes<128>(rows, num_sms)
+                      : attn_workspace_bytes<256>(rows, num_sms);
 }
 
 }  // namespace
@@ -304,15 +268,16 @@ FA2_EXPORT fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o,
     const fa2::cache::Device dev(c->k);
     if (dev.status() != FA2_OK)
         return dev.status();
-    a.num_sms = fa2::cache::sm_count(dev.id());
+    a.num_sms = fa2::sm_count(dev.id());
     a.err = fa2::cache::device_error_ptr(dev.id());
     a.naps = fa2::cache::test_naps();
-    a.drain_limit_ns = fa2::cache::wait_limit_ns();
-    a.wait_limit_ns = fa2::cache::call_wait_limit_ns();
+    a.drain_limit_ns = fa2::wait_limit_ns();
+    a.wait_limit_ns = fa2::call_wait_limit_ns();
     if (a.num_sms <= 0 || !a.err)
         return FA2_ERR_CUDA;
-    return c->D == 64 ? fa2::cache::launch_attn_d64(a)
-                      : c->D == 128 ? fa2::cache::launch_attn_d128(a) : fa2::cache::launch_attn_d256(a);
+    return c->D == 64    ? fa2::cache::launch_attn<64>(a)
+           : c->D == 128 ? fa2::cache::launch_attn<128>(a)
+                         : fa2::cache::launch_attn<256>(a);
 }
 
 FA2_EXPORT fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq, int D, int device, size_t *bytes)
@@ -327,7 +292,7 @@ FA2_EXPORT fa2_status fa2_cache_attn_workspace_size(int B, int Hq, int H, int Lq
         return FA2_ERR_UNSUPPORTED;
     if (Lq == 0)
         return FA2_OK;
-    const int sms = fa2::cache::sm_count(device);
+    const int sms = fa2::sm_count(device);
     if (sms <= 0)
         return FA2_ERR_CUDA;
     *bytes = fa2::cache::workspace_bytes(D, static_cast<long long>(Lq) * (Hq / H), sms);
