@@ -1,10 +1,10 @@
 // fa2_cache_move.cu -- fa2_cache_write and fa2_cache_read: bf16 rows into and out of
 // the paged e4m3 cache.  Both only move bytes (3 per value: 2 bf16, 1 code); a code
 // and its scale determine the value exactly, so nothing here rounds but the one
-// conversion to e4m3.  Measured: eight prompts of up to 8192 rows, 8 heads of 128, 302 MB
-// in 46 us, 6.6 TB/s; four contexts of 16384, 16 heads of 128, 805 MB out in 122 us, 6.6
-// TB/s: the measured copy rate but for 2 %.  One row a sequence (128 of them, part
-// of a page each) and short prefixes are launches: 3.1 us.
+// conversion to e4m3.  Measured (three inputs in turn): eight prompts of up to 8192 rows, 8
+// heads of 128, 302 MB in 48 us, 6.3 TB/s; four contexts of 16384, 16 heads of 128, 805 MB
+// out in 124.5 us, 6.5 TB/s: 93 and 95 % of the measured copy rate.  One row a sequence (128
+// of them, part of a page each) and short prefixes are launches: 2.7 and 2.9 us.
 #include <climits>
 
 #include "fa2_cache.cuh"

@@ -22,7 +22,10 @@
 // O^T is added to fp32 registers times 2^(m - M), M the largest m so far, and
 // l += 2^-ev p likewise.  Every tile has a reference of its own, so the terms' small range
 // never meets the spread of scores over a long context, and since the references are whole
-// numbers the factors are exact.
+// numbers the factors are exact.  l sums the weights as they are before their rounding: LSE
+// needs that sum, and one of the rounded weights for O alone, in which the rounding of a key
+// that dominates would cancel (2^-11 at most, under bf16's 2^-8), would cost R registers and
+// the additions.
 //
 // What bounds it.  One token of a group of 8 does 16 operations a cache byte, the card
 // could do 290: the bytes are the time, and no other unit may come near it.  The codes are
@@ -32,12 +35,15 @@
 // that one's softmax runs under the other's products (D = 128, 16 rows, 131 MB of cache: 49
 // us, 61 with one; D = 64, 8 rows: 41 with three, 43 with two).  Work is cut and merged as
 // in fa2_cache_line.cuh.
-// Measured: one token of 48 sequences of 64 to 8192 positions, 8 heads of 128, groups of 4:
-// 407 MB in 69 us, 5.9 TB/s, 88 % of the measured copy rate; of two of 125000: 514 MB in 84
-// us, 6.1 TB/s.  At D = 64 a tile holds half the bytes for the same softmax, and that bounds
-// it: 16 sequences of 6000, 8 heads, 98 MB in some 37 us.  Short calls are latency: of 14 us
-// for 34 MB (a window of 1024 in 16 sequences), 2 go to the launch, 1.5 to laying out the
-// line, 1 to q, 2 to merging parts.
+// Measured (several inputs in turn, so that none is in L2): one token of 48 sequences of 64 to
+// 8192 positions, 8 heads of 128, groups of 4: 407 MB in 70.6 us, 5.8 TB/s, 85 % of the
+// measured copy rate; of two of 125000: 514 MB in 85.5 us, 6.0 TB/s; D = 256, 16 of 16000, 4
+// heads, groups of 8: 525 MB in 88 us, 5.9 TB/s, and 8 of 8000, 8 heads: 262 MB in 49.5, 5.3.
+// At D = 64 a tile holds half the bytes for the same softmax, and that bounds it: 16 sequences
+// of 24000, 8 heads, groups of 8, 394 MB in 102 us, 3.9 TB/s, and of 6000 98 MB in 34, 2.9.  So
+// does twice the softmax for 16 rows: D = 128, 16 of 4000, 132 MB in 42.6 us, 3.1 TB/s.  Short
+// calls are latency: of 14 us for 34 MB in L2 (a window of 1024 in 16 sequences; 17 from
+// memory), 2 go to the launch, 1.5 to laying out the line, 1 to q, 2 to merging parts.
 #pragma once
 
 #include <atomic>
