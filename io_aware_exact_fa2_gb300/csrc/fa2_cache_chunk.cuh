@@ -115,6 +115,10 @@ struct ChunkCfg {
     static_assert(SMEM_BYTES + 1024 + 1024 <= 228 * 1024 && NQ * (TILE + D + (P_APART ? P_STEP : 0)) <= TMEM_COLS, "an SM holds it");
 };
 
+// Scores (times log2 e) past which a row's reference is too coarse for what is subtracted from it
+// exactly: its last place is 2^-3 there.
+constexpr float LARGE = 1 << 20;
+
 // Error codes of waits that ran out (bits 8-11 the waiting role).
 constexpr int CHUNK_ERR_SOFTMAX = 8 << 8, CHUNK_ERR_CONVERT = 9 << 8, CHUNK_ERR_MMA = 10 << 8, CHUNK_ERR_LOAD = 11 << 8,
               CHUNK_ERR_DRAIN = 7 << 8;
@@ -702,12 +706,13 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                     }
                 };
                 // Weights as f16 pairs, by the maximum so far.  Their sum tells whether one is
-                // too large for it: only then (and for a row's first keys) is the tile's maximum
-                // taken, O and l brought to it, and the weights taken again.
+                // too large for it: only then (and for a row's first keys, and scores past LARGE) is
+                // the tile's maximum taken, O and l brought to it, and the weights taken again.
                 uint32_t p[32];
                 float sum, add_l;
                 bool waited = fresh;
-                bool again = __any_sync(0xffffffffu, M == -INFINITY && lo < pos0 + TILE && hi > pos0);
+                float ref = 6.f - (M == -INFINITY ? 0.f : M);
+                bool again = __any_sync(0xffffffffu, fabsf(M) > LARGE);   // (or no maximum yet)
                 for (int attempt = 0; attempt < 2; ++attempt) {
                     if (again) {
                         float top = -INFINITY;   // of x + ev
@@ -745,6 +750,30 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                                 tmem_st16(o_addr + 16 * cc, o);
                             }
                         }
+                        // M is rounded, and S c + ev - M below is not: at scores past 2^20 the two would
+                        // be apart by more than a little.  There the scores become those of x - M, x + ev
+                        // rounded as M was, where they are, and the reference 0.  (M is the tile's own
+                        // maximum or above it by now, so no further attempt finds them changed.)
+                        const bool moved = fabsf(M) > LARGE && M != -INFINITY;
+                        ref = 6.f - (M == -INFINITY || moved ? 0.f : M);
+                        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
+                            for (int i = 0; i < TILE / 8; ++i) {   // (four at a time: registers)
+                                uint32_t r[4];
+                                tmem_ld(s_addr + half * C::HALF + i * 4, r);
+                                tmem_wait_ld();
+                                tmem_pin(r);
+                                const float4 scales = info[half * (GROUPS / 2) + i / 4];
+                                const float c = fmaxf(scale_row * scales.x, 1.17549435e-38f), inv = rcp_approx(c);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float x = (fmaf(__uint_as_float(r[k]), c, scales.y) - M - scales.y) * inv;
+                                    r[k] = moved ? __float_as_uint(x) : r[k];
+                                }
+                                tmem_st(s_addr + half * C::HALF + i * 4, r);
+                            }
+                            tmem_st_wait();
+                        }
                     }
                     // weights apart go where the tile before's were, as they are made
                     if (C::P_APART && !waited) {
@@ -752,7 +781,6 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
                         waited = true;
                         tc_fence_after();
                     }
-                    const float ref = 6.f - (M == -INFINITY ? 0.f : M);
                     sum = add_l = 0.f;
                     for_groups([&](int i, const uint32_t (&r)[CHUNK], float c, float ev, float lf) {
                         const float add = ev + ref;

@@ -112,3 +112,37 @@ def test_value_scales_far_apart(D, rows, apart, workspace):
         bound = 2.0 ** -8 * np.abs(want[0, r, 0]) + (1 + 2.0 ** -8) * ((2.0 ** -11 + 2 * ds + n * 2.0 ** -22) * mass[0, r, 0] + small)
         over = np.abs(o[0, r, 0].double().cpu().numpy() - want[0, r, 0]) - bound
         assert over.max() <= 0, f"row {r}: {over.max():.3e} over its bound"
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,Lq", ROWS)
+@pytest.mark.parametrize("log2", [8, 18, 24, 30, 40, 90])
+@pytest.mark.parametrize("lens,workspace", [([300, 90], False), ([1500, 700], True)])
+def test_large_scores_of_any_bits(D, G, Lq, log2, lens, workspace):
+    """Scores of all 24 bits, some 2^log2 large: the greatest one's value is the answer wherever the
+    next is further below than the scores' own error (2 D additions' and q's terms', as
+    cache_reference.attention derives it) and what a weight can still show."""
+    c = Cache(len(lens), 1, D, 16, lens, seed=D + G + log2, nan_after=False)
+    c.ks[:] = 120
+    q = ref.bf16(c.rng.standard_normal((2, G, Lq, D)) * 2.0 ** log2)
+    o, lse = attend(c, G, Lq, lens, q=q, workspace=workspace, check=False)
+    o, lse, qn, seen = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy(), 0
+    for b, n in enumerate(lens):
+        k, _ = ref.gather(c.k, c.ks, c.table[b], 0, n)
+        v, _ = ref.gather(c.v, c.vs, c.table[b], 0, n)
+        for g in range(G):
+            for i in range(Lq):
+                row, m = qn[b, g, i], n - Lq + i + 1
+                s = k[:m] @ row * D ** -0.5
+                first, second = s.argmax(), np.partition(s, -2)[-2]
+                reach = (np.abs(k[:m]) @ np.abs(row)).max() * D ** -0.5
+                ds = reach * 2 * D * 2.0 ** -23 + 2.0 ** -21 * (1 + np.abs(s).max()) + \
+                    D ** -0.5 * 2.0 ** (-21 if G * Lq <= 16 else -17) * np.abs(row).max() * np.abs(k[:m]).sum(1).max()
+                if s[first] - second < 2 * ds + 40:      # e^-40: nothing of the next one's value
+                    continue
+                seen += 1
+                assert abs(lse[b, g, i] - s[first]) <= ds + 2.0 ** -21 * (1 + abs(s[first]))
+                # (a weight is off by 2^-11, O by 2^-8 of itself)
+                d = np.abs(o[b, g, i] - v[first]) - (2.0 ** -8 + 2.0 ** -10) * np.abs(v[first])
+                assert d.max() <= 2.0 ** -30, f"sequence {b}, head {g}, row {i}: {d.max():.3e} over its bound"
+    assert seen >= 0.6 * len(lens) * G * Lq or log2 < 18   # (where the next is often too near)
