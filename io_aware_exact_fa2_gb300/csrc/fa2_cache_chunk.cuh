@@ -14,7 +14,8 @@
 // accumulator takes pages of any strength.  P' is f16 (two terms of e4m3 would not span a
 // long context's weights) and V is converted to f16, exactly.  M is raised only when the
 // weights that a tile has by it would leave f16's range, which their sum tells: most tiles
-// need no maximum at all.  l sums the weights before their rounding to f16, 2^-11 at most: LSE
+// need no maximum at all.  (Past 2^20 the multiply-add is exact where M is rounded: there a
+// tile's scores are replaced by their differences from its maximum first.)  l sums the weights before their rounding to f16, 2^-11 at most: LSE
 // needs that sum, and one of the rounded weights for O alone would cost a conversion back of
 // each.
 //
@@ -31,7 +32,7 @@
 //     1 warp         pages into shared memory by TMA
 // on one CTA an SM.  Work is cut and merged as in fa2_cache_line.cuh.
 // Measured (several inputs in turn, so that none is in L2): 2048 tokens at the end of 16384, 32
-// heads on 8 of 128: 515 GFLOP in 383 us, 1346 TFLOP/s, 70 % of the measured bf16 rate, the
+// heads on 8 of 128: 515 GFLOP in 377 us, 1366 TFLOP/s, 71 % of the measured bf16 rate, the
 // tensor pipe busy for 58 % of the cycles; no unit is saturated (issue slots 51 %): a row
 // tile's chain of products, scores, exponentials and weights, some 3600 cycles for 256 rows by
 // 128 keys, has only the other tile's to hide under.  That is not the limit of two row tiles:
@@ -40,9 +41,9 @@
 // vote of two warps before a weight may be stored, two threads a row, converted values.  With
 // two CTAs of one row tile an SM, which convert the values twice: 499 us.  One thread a row
 // instead of two: 435 us.  At D = 64 the chain is as long for half the work: 258 GFLOP of the
-// same lengths in 300 us, six ragged prompts' chunks, 24.5 GFLOP, in 59.  At D = 256, 16 heads
-// on 4: 515 GFLOP in 483 us, 1067 TFLOP/s.  Units of up to 128 rows take as long as full ones:
-// 32 rows, 16 sequences of 4000, 8 heads of 128, 133 MB in 55 us for a floor of 20.
+// same lengths in 300 us, six ragged prompts' chunks, 24.5 GFLOP, in 60.  At D = 256, 16 heads
+// on 4: 515 GFLOP in 482 us, 1069 TFLOP/s.  Units of up to 128 rows take as long as full ones:
+// 32 rows, 16 sequences of 4000, 8 heads of 128, 133 MB in 54 us for a floor of 20.
 #pragma once
 
 #include <atomic>

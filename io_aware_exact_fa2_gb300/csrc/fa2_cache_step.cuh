@@ -36,9 +36,9 @@
 // us, 61 with one; D = 64, 8 rows: 41 with three, 43 with two).  Work is cut and merged as
 // in fa2_cache_line.cuh.
 // Measured (several inputs in turn, so that none is in L2): one token of 48 sequences of 64 to
-// 8192 positions, 8 heads of 128, groups of 4: 407 MB in 70.6 us, 5.8 TB/s, 85 % of the
-// measured copy rate; of two of 125000: 514 MB in 85.5 us, 6.0 TB/s; D = 256, 16 of 16000, 4
-// heads, groups of 8: 525 MB in 88 us, 5.9 TB/s, and 8 of 8000, 8 heads: 262 MB in 49.5, 5.3.
+// 8192 positions, 8 heads of 128, groups of 4: 407 MB in 70 us, 5.8 TB/s, 86 % of the
+// measured copy rate; of two of 125000: 514 MB in 84.5 us, 6.1 TB/s; D = 256, 16 of 16000, 4
+// heads, groups of 8: 525 MB in 87.6 us, 6.0 TB/s, and 8 of 8000, 8 heads: 262 MB in 48.9, 5.4.
 // At D = 64 a tile holds half the bytes for the same softmax, and that bounds it: 16 sequences
 // of 24000, 8 heads, groups of 8, 394 MB in 102 us, 3.9 TB/s, and of 6000 98 MB in 34, 2.9.  So
 // does twice the softmax for 16 rows: D = 128, 16 of 4000, 132 MB in 42.6 us, 3.1 TB/s.  Short
