@@ -146,7 +146,7 @@ fa2_status fa2_cache_read(const fa2_cache *c, void *k, void *v, const long long 
  *              all.  Rows i >= q_lens[b] of o and lse are left as they were.
  *   Hq         query heads, a multiple of c->H.
  *   Lq         query rows a sequence (0: no-op); Lq * Hq / H at most 2^30.
- *   scale      finite and > 0.
+ *   scale      > 0, and finite times log2 e (below 2.358e38).
  *   workspace  optional device workspace (256-byte aligned, fa2_cache_attn_workspace_size
  *              bytes, ZERO-FILLED before its first use, left ready by every
  *              completed call).  With it the keys of one sequence are shared out

@@ -241,7 +241,7 @@ FA2_EXPORT fa2_status fa2_cache_attn(const fa2_cache *c, const void *q, void *o,
     if (Hq <= 0 || Hq % c->H != 0 || Lq < 0 || static_cast<long long>(c->B) * Hq > INT_MAX ||
         static_cast<long long>(Lq) * (Hq / c->H) > fa2::cache::kMaxLength)
         return FA2_ERR_INVALID_ARG;
-    if (!std::isfinite(scale) || !(scale > 0.f) || window < -1 || (window >= 0 && !causal))
+    if (!std::isfinite(scale * 1.4426950408889634f) || !(scale > 0.f) || window < -1 || (window >= 0 && !causal))
         return FA2_ERR_INVALID_ARG;
     if (!fa2::cache::row_strides(q_strides, Hq, Lq, c->D, a.q_sb, a.q_sh, a.q_sl) ||
         !fa2::cache::row_strides(o_strides, Hq, Lq, c->D, a.o_sb, a.o_sh, a.o_sl))

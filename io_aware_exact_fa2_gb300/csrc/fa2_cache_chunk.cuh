@@ -15,9 +15,9 @@
 // long context's weights) and V is converted to f16, exactly.  M is raised only when the
 // weights that a tile has by it would leave f16's range, which their sum tells: most tiles
 // need no maximum at all.  (Past 2^20 the multiply-add is exact where M is rounded: there a
-// tile's scores are replaced by their differences from its maximum first.)  l sums the weights before their rounding to f16, 2^-11 at most: LSE
-// needs that sum, and one of the rounded weights for O alone would cost a conversion back of
-// each.
+// tile's scores are replaced by their differences from its maximum first.)  l sums the weights
+// before their rounding to f16, 2^-11 at most: LSE needs that sum, and one of the rounded
+// weights for O alone would cost a conversion back of each.
 //
 // What bounds it.  4 D operations a (row, key) pair against D / 64 cache bytes a row and
 // key: the tensor pipe.  (Two e4m3 products take the time of one of f16, and K needs no

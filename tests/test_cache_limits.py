@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from test_cache_abi import CUDA_ERR, UNSUPPORTED, P, cache, lib, ll3, write   # noqa: F401 (lib: a fixture)
+from test_cache_abi import CUDA_ERR, INVALID, UNSUPPORTED, P, attn, cache, lib, ll3, write   # noqa: F401 (lib: a fixture)
 
 
 # pages that L rows can touch, or pieces of 8192 / D rows; keys and values; B H heads: 2^31 - 1 at most
@@ -21,3 +21,10 @@ def test_more_blocks_than_a_launch_counts_are_refused(lib, f, D, page, L, heads_
     assert write(lib, cache(lib, B=heads_over, H=1, D=D, page_size=page, **strides), ks=rows, vs=rows, L=L, f=f) == UNSUPPORTED
     if not torch.cuda.is_available():   # (the pointers are not real)
         assert write(lib, cache(lib, B=heads_in, H=1, D=D, page_size=page, **strides), ks=rows, vs=rows, L=L, f=f) == CUDA_ERR
+
+
+@pytest.mark.parametrize("scale", [2.36e38, 3.4e38])
+def test_a_scale_that_log2_e_takes_past_fp32_is_refused(lib, scale):   # noqa: F811
+    assert attn(lib, cache(lib), scale=scale) == INVALID
+    if not torch.cuda.is_available():
+        assert attn(lib, cache(lib), scale=2.35e38) == CUDA_ERR
