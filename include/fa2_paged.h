@@ -149,6 +149,9 @@ fa2_status fa2_paged_append(const fa2_paged *c, const void *k, const void *v, co
  * is more); for more rows to one term, off by 2^-9 and 2^-12 on average and 2^-8 and
  * 2^-11 at most.  For those bf16 O is divided by the sum of the rounded weights (where one
  * key dominates, its rounding cancels); LSE, and all else, takes the sum before.
+ * O is finite where values are, unless a column's sum_j exp(s_ij - max_j s_ij) |V_j| is 2^131
+ * or more (for bf16 values of that size only: 8 keys alike of the largest finite value, any
+ * number of 2^101).  A key's part in it counts down to 2^-137 (bf16).
  *
  *   q          16-bit [B, Hq, Lq, D] device view, strides (batch, head, row) or NULL.
  *   o          16-bit [B, Hq, Lq, D] device view (written), likewise; its rows must not

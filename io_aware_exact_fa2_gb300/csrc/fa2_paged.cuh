@@ -43,6 +43,18 @@ struct MoveArgs {                   // fa2_rope, fa2_paged_append
     int append;                     // rows past counts are not read
 };
 
+// A weight is 2^LIFT of the type where its score is the row's reference (a score up to 8 below its
+// largest, in the exponent), and UNIT is that number.
+// fp16: weights up to 2^14, of which the type keeps those 2^-31 below the largest's.
+// bf16 has the range of fp32, in which O is held until it is divided: weights up to 2^-4, so that a row's
+// sum stays finite with values of any finite size, unless sum_j exp(s_j - max) |v_j| passes 2^131 (a
+// reference past 2^24 may be off by 1: fa2_paged_chunk.cuh), and small ones up to 2^-114 below the
+// reference's still count.  (With 6, values of 2^122 made O infinite over one key.)
+template <bool F16>
+struct Weight {
+    static constexpr float LIFT = F16 ? 6.f : -12.f, UNIT = F16 ? 64.f : 1.f / 4096;
+};
+
 // Blocks of a move, which a launch counts in an int.
 long long move_blocks(const MoveArgs &a);
 fa2_status launch_move(const MoveArgs &a, bool f16, cudaStream_t stream);

@@ -73,7 +73,7 @@ struct ChunkCfg {
     // quarter of which on average shows in O (and adding fp16 to fp32 takes twice the issue slots
     // of bf16: six ragged prompts' chunks at D = 64 66 us with it, 59 without).
     static constexpr bool SEEN = !F16;
-    static constexpr float LIFT = 6.f;               // weights up to 2^14: fp16 keeps those 2^-31 below 1
+    static constexpr float LIFT = Weight<F16>::LIFT;
 
     // A tile's keys, and its values, are PARTS slots of the ring, of up to 128 columns each, in
     // panels of 64 columns (128 bytes a row, the swizzle's span).
@@ -147,8 +147,9 @@ __device__ __forceinline__ float reference(float M, float c)
 template <class C>
 __device__ __forceinline__ float left_out(float M, float c)
 {
-    const float x = __fmul_rn(M, c);
-    return fmaf(M, c, -x) + ((x - __fsub_rn(x, C::LIFT)) - C::LIFT);
+    const float x = __fmul_rn(M, c), y = __fsub_rn(x, C::LIFT);
+    const float lift = __fsub_rn(x, y);   // what of LIFT went into y; what of x: y + lift
+    return fmaf(M, c, -x) + (__fsub_rn(x, __fadd_rn(y, lift)) + __fsub_rn(lift, C::LIFT));
 }
 // 2^(from - to): what is relative to one reference, brought to another.
 template <class C>
@@ -904,7 +905,7 @@ __global__ void __launch_bounds__(C::T, 1)
             const float inv = l_seen == 0.f ? 0.f : 1.f / l_seen;
             // log2 of the weights' sum, relative to M c itself
             const float y = l == 0.f ? -INFINITY
-                                     : lg2_approx(l) - C::LIFT - (fabsf(reference<C>(M, c)) > LARGE ? 0.f : left_out<C>(M, c));
+                                     : lg2_approx(l * (1.f / Weight<F16>::UNIT)) - (fabsf(reference<C>(M, c)) > LARGE ? 0.f : left_out<C>(M, c));
             const Row at = this_row();
             uint16_t *const o = static_cast<uint16_t *>(a.o) + line.b * a.o_sb;
             const long long o_place = at.live ? at.hq * a.o_sh + at.tok * a.o_sl : -1;

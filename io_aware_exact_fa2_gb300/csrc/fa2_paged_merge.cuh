@@ -2,12 +2,13 @@
 // put together: fa2_paged_step.cuh and fa2_paged_chunk.cuh.
 //
 // A part says what it computed as O / l and two floats: M, a score as the products gave it, and
-// y = log2 l - LIFT, where l sums 2^((S - M) c + LIFT).  Scores stay scores: a difference of two
-// M times c is exact where it matters, whatever their size, where M c as a float would be off by
-// 2^-24 of it, 2^19 at scores of 2^43.
+// y = log2 of the sum of 2^((S - M) c).  Scores stay scores: a difference of two M times c is exact
+// where it matters, whatever their size, where M c as a float would be off by 2^-24 of it, 2^19 at
+// scores of 2^43.  Parts count by weights of the same size as a key's (Weight::UNIT).
 #pragma once
 
 #include "fa2_cache_line.cuh"
+#include "fa2_paged.cuh"
 
 namespace fa2 {
 namespace paged {
@@ -58,7 +59,7 @@ __device__ __forceinline__ float merge_row(const cache::Parts &parts, float c, i
             v[k].x *= f, v[k].y *= f, v[k].z *= f, v[k].w *= f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float g = ptx::ex2_approx(fmaf(sum[w].x - top, c, sum[w].y));
+            const float g = ptx::ex2_approx(fmaf(sum[w].x - top, c, sum[w].y)) * Weight<C::F16>::UNIT;
             l += g;
 #pragma unroll
             for (int k = 0; k < N; ++k)
@@ -69,7 +70,7 @@ __device__ __forceinline__ float merge_row(const cache::Parts &parts, float c, i
 #pragma unroll
     for (int k = 0; k < N; ++k)
         v[k].x *= inv, v[k].y *= inv, v[k].z *= inv, v[k].w *= inv;
-    return l == 0.f ? -INFINITY : log2_sum(top, c, ptx::lg2_approx(l));
+    return l == 0.f ? -INFINITY : log2_sum(top, c, ptx::lg2_approx(l * (1.f / Weight<C::F16>::UNIT)));
 }
 #endif
 

@@ -65,7 +65,7 @@ struct StepCfg {
     static constexpr bool REG_SPLIT = NW == 2;
     static constexpr int REG_SOFTMAX = 216, REG_CTRL = 72;
     static_assert(2 * REG_SOFTMAX + REG_CTRL <= 3 * 168, "the split draws on the launch's registers");
-    static constexpr float LIFT = 6.f, SLACK = 8.f;  // weights up to 2^14: fp16 keeps those 2^-31 below the reference's
+    static constexpr float LIFT = Weight<F16>::LIFT, SLACK = 8.f;
 
     // A tile's keys, and its values, are PARTS slots of the ring, of up to 128 columns each, in
     // panels of 64 columns (128 bytes a row, the swizzle's span).
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(C::T, C::CTAS)
             if (key < RW) {
                 const float sum = sum_of(key);
                 if (sum != 0.f)
-                    y = lg2_approx(sum) - C::LIFT;
+                    y = lg2_approx(sum * (1.f / Weight<F16>::UNIT));
             }
             const float M = sh_ref[key < RW ? key : 0];
             uint16_t *const o = static_cast<uint16_t *>(a.o);
