@@ -8,7 +8,8 @@
 //     p_j = 2^(S_j c - M c + LIFT),   P = p in the cache's type,   O += P V,   l += p,   l' += P
 // O and l are brought to a larger M only when a tile's scores pass it by more than 8 in the
 // exponent.  O is divided by l', the sum of the weights that the product saw, so that a weight's
-// rounding cancels where one key dominates; LSE and a part's share in a row come from l.  The
+// rounding cancels where one key dominates (fp16, and bf16 at D = 256, where P is two terms: by l);
+// LSE and a part's share in a row come from l.  The
 // reference is the float F = M c - LIFT, whatever it was rounded by, and 2^(S_j c - F) one
 // multiply-add.  Where |F| passes 2^25 its rounding could leave the range of a weight: there the
 // scores are replaced by S_j - M first, where they are, and the reference is M c - LIFT itself.
@@ -28,8 +29,8 @@
 // Measured.  2048 tokens of a prompt over 16384 keys, theirs included, 32 and 8 heads of 128,
 // causal (515 GFLOP): 333 to 343 us, 1.50 to 1.55 PFLOP/s, 0.79 to 0.81 of the measured matrix
 // rate; the loop over tiles shifts by 3 % with any change of its code.  The same with heads of 64
-// (as many exponentials for half the products) 280 us; 16 and 4 heads of 256 388 us; pages of 16
-// keys 346.  No single unit is the bound: in timing copies, without the exponentials 334 us for
+// (as many exponentials for half the products) 282 us; 16 and 4 heads of 256 478 us, fp16 384;
+// pages of 16 keys 347.  No single unit is the bound: in timing copies, without the exponentials 334 us for
 // 360, with half the bytes of K and V 341 for 354.
 // Five drafted tokens of 24 contexts of up to 4096 keys, 16 and 2 heads of 64 (26 MB), 20.5 us:
 // a launch, the lengths, one or two units of half-filled tiles a CTA, and the merge.
@@ -72,7 +73,12 @@ struct ChunkCfg {
     // Whether l' is summed: a bf16 weight is off by 2^-8, as O itself, an fp16 one by 2^-11, a
     // quarter of which on average shows in O (and adding fp16 to fp32 takes twice the issue slots
     // of bf16: six ragged prompts' chunks at D = 64 66 us with it, 59 without).
-    static constexpr bool SEEN = !F16;
+    static constexpr bool SEEN = !F16 && D < 256;
+    // bf16 weights at D = 256 are two terms, as in the dense pass: with one, where two or three keys stand
+    // out alike, 9 of 8.2 M values around 2.3 were off by more than 1e-2 (2 x 8 heads, 2000 rows of 3000 keys,
+    // every 64th of them eight times as large), with two none but by their own rounding.  It costs one more
+    // product: the prompt chunk at D = 256 478 us, 388 with one (fp16, which has one, 384).
+    static constexpr bool TWO = !F16 && D == 256;
     static constexpr float LIFT = Weight<F16>::LIFT;
 
     // A tile's keys, and its values, are PARTS slots of the ring, of up to 128 columns each, in
@@ -88,6 +94,8 @@ struct ChunkCfg {
     static constexpr int TM_S = 0, TM_O = NQ * NS * TILE, TM_P = P_APART ? TM_O + NQ * D : TM_S, P_STEP = P_APART ? TILE / 2 : TILE;
     static constexpr int TMEM_COLS = 512;
     static_assert(TM_O + NQ * D + (P_APART ? NQ * P_STEP : 0) <= TMEM_COLS, "tensor memory holds it");
+    static constexpr int P_LOW = TILE / 2;           // the second term's columns behind the first's
+    static_assert(!TWO || !P_APART, "both terms lie over the scores");
 
     static constexpr int OFF_Q = 0, OFF_RING = NQ * Q_TILE, MARK_WORDS = D / 32;
     static constexpr int OFF_MARK = OFF_RING + SLOTS * SLOT;         // values of O that are NaN, by row
@@ -402,8 +410,11 @@ __global__ void __launch_bounds__(C::T, 1)
                             const uint64_t dv = desc_v + (slot * C::SLOT >> 4);
 #pragma unroll
                             for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                                mma_ts(tmem + C::TM_O + q * D + part * C::DP, p + kk * 8, dv + (kk * 16 * 128 >> 4),
-                                       idesc(F16, 128, C::DP, false, true), !start || kk > 0);
+#pragma unroll
+                                for (int term = 0; term < (C::TWO ? 2 : 1); ++term)
+                                    mma_ts(tmem + C::TM_O + q * D + part * C::DP, p + term * C::P_LOW + kk * 8,
+                                           dv + (kk * 16 * 128 >> 4), idesc(F16, 128, C::DP, false, true),
+                                           !start || kk > 0 || term > 0);
                             if (half && last_v)
                                 mma_commit(bar(C::BAR_EMPTY + slot));
                         }
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(C::T, 1)
             __syncwarp();
         } else if (warp == C::WARP_LOAD || warp == C::WARP_V) {
             // ======================================== pages -> ring: keys' by one warp, values' by another
-            // (one warp for both: 570 us instead of 388 for the prompt chunk at D = 256, 391 instead of 346
+            // (one warp for both: 570 us instead of 388 for the prompt chunk at D = 256, one term a weight, 391 instead of 346
             // over pages of 16 at D = 128)
             const bool values = warp == C::WARP_V;
             const CUtensorMap *const map = values ? &v_map : &k_map;
@@ -832,7 +843,7 @@ __global__ void __launch_bounds__(C::T, 1)
                 const uint64_t c2 = f32x2(c, c), add2 = f32x2(plus, plus);
                 auto weights = [&](auto half) {
                     constexpr int H = decltype(half)::value;
-                    uint32_t p[32];
+                    uint32_t p[32], low[C::TWO ? 32 : 1];
 #pragma unroll
                     for (int k = 0; k < 64; k += 4) {
                         const float *const x = s + H * 64 + k;
@@ -848,8 +859,17 @@ __global__ void __launch_bounds__(C::T, 1)
                             seen[0] = add_bf16x2_to_f32(seen[0], p[k / 2]);
                             seen[1] = add_bf16x2_to_f32(seen[1], p[k / 2 + 1]);
                         }
+                        if constexpr (C::TWO) {
+                            float z0, z1, z2, z3;
+                            unpack2<F16>(p[k / 2], z0, z1);
+                            unpack2<F16>(p[k / 2 + 1], z2, z3);
+                            low[k / 2] = pack2<F16>(p0 - z0, p1 - z1);
+                            low[k / 2 + 1] = pack2<F16>(p2 - z2, p3 - z3);
+                        }
                     }
                     tmem_st32(p_addr + H * 32, p);
+                    if constexpr (C::TWO)
+                        tmem_st32(p_addr + C::P_LOW + H * 32, low);
                 };
                 weights(std::integral_constant<int, 0>{});
                 tmem_st_wait();

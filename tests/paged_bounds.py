@@ -13,7 +13,7 @@ from paged_reference import HALF, TINY
 
 def two_terms(D, rows, dtype):
     """Whether a weight goes into the product with V as two terms: `rows` query rows a key/value head."""
-    return rows <= (16 if D == 256 else 32)
+    return rows <= (16 if D == 256 else 32) or (D == 256 and dtype == torch.bfloat16)
 
 
 def _heads(q, c, kv_lens, q_lens, causal, scale):

@@ -31,6 +31,14 @@ def test_a_lost_second_term_shows(D, rows, dtype):
     assert not passes(c, q, [48], scale, terms=1, lift=lift)
 
 
+def test_wide_bf16_heads_have_two_terms_for_any_rows():
+    c = Cache(1, 1, 256, 16, [48], seed=1, dtype=BF16, odd_after=False)
+    q = c.randn(1, 1, 40, 256).to(BF16)
+    scale = bounds.few_alike(c, q, 1)
+    assert passes(c, q, [48], scale, terms=2, lift=-12.0)
+    assert not passes(c, q, [48], scale, terms=1, lift=-12.0)
+
+
 @pytest.mark.parametrize("rows,terms", [(40, 1), (8, 2)])
 def test_small_fp16_weights_need_the_lift(rows, terms):
     c = Cache(1, 1, 64, 16, [700], seed=rows, dtype=FP16, odd_after=False)

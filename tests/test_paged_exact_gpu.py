@@ -51,6 +51,16 @@ def test_17_to_32_rows_have_two_terms(D, dtype, G, Lq):
     check(c, q, lens, causal=False, scale=bounds.few_alike(c, q, G))
 
 
+@pytest.mark.parametrize("Lq", [1, 20, 33, 140])
+def test_wide_bf16_heads_have_two_terms(Lq):
+    """D = 256: as the dense pass has them, for any number of rows."""
+    lens = [700, 257, 140]
+    c = Cache(3, 1, 256, 32, lens, seed=Lq, dtype=BF16, odd_after=False)
+    q = c.randn(3, 2, Lq, 256).to(BF16)
+    check(c, q, lens)
+    check(c, q, lens, causal=False, scale=bounds.few_alike(c, q, Lq))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("Lq", [1, 5, 40, 300])
@@ -97,10 +107,10 @@ def test_values_of_any_size_in_parts(D, Lq, power):
     check(c, q, lens, [Lq, min(Lq, 60)])
 
 
-@pytest.mark.parametrize("name,mode", [("c2", "noncausal"), ("c3", "causal")])
+@pytest.mark.parametrize("name,mode", [("c2", "noncausal"), ("c3", "causal"), ("c5", "noncausal")])
 def test_dense_workloads_through_the_cache(name, mode):
     """Appended to a cache and attended to by all their queries at once, to the dense forward's bar: 1e-2, and
-    half a step of O's where |O| >= 4."""
+    half a step of O's where |O| >= 4.  (c5: D = 256, every 64th key eight times as large.)"""
     import io_aware_exact_fa2_gb300 as fa2
     w = WORKLOADS[name]
     q, k, v = workload_inputs(w)
