@@ -1,7 +1,7 @@
 """Build the CUDA libraries in-tree: io_aware_exact_fa2_gb300/libfa2_gb300.so (the
 dense passes, include/fa2.h), libfa2_cache_gb300.so (the 8-bit cache, include/fa2_cache.h)
 and libfa2_paged_gb300.so (the 16-bit cache and the position rotation, include/fa2_paged.h),
-with the Python module that hands tensors to the last.
+then, where there is a torch with CUDA, the Python module that hands tensors to the last.
 
 nvcc compiles each translation unit in csrc/ for sm_103a (in parallel), then
 links the shared libraries with the CUDA runtime linked statically and only the
@@ -60,15 +60,31 @@ def nvcc() -> str:
 
 
 def source_digest() -> str:
-    """Hash of every kernel/host source and the public headers (for staleness checks)."""
+    """Hash of the libraries' sources and the public headers (for staleness checks)."""
     h = hashlib.sha256()
-    files = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp")))
+    files = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
     for f in files:
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())
-    h.update(f"{sys.version} torch {importlib.metadata.version('torch')}".encode())   # (PY_SOURCE is built against both)
     for f in ("fa2.h", "fa2_cache.h", "fa2_paged.h"):
         with open(os.path.join(INCLUDE, f), "rb") as fh:
+            h.update(fh.read())
+    return h.hexdigest()[:16]
+
+
+def torch_with_cuda() -> str | None:
+    """The folder of this Python's torch (found, not imported: that takes seconds); None if there is
+    none, or one without CUDA."""
+    spec = importlib.util.find_spec("torch")
+    path = os.path.dirname(spec.origin) if spec and spec.origin else None
+    return path if path and os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
+def module_digest() -> str:
+    """Hash of the module's source and headers, and of what it is built against."""
+    h = hashlib.sha256(f"{sys.version} torch {importlib.metadata.version('torch')}".encode())
+    for f in (os.path.join(CSRC, PY_SOURCE), os.path.join(INCLUDE, "fa2.h"), os.path.join(INCLUDE, "fa2_paged.h")):
+        with open(f, "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
 
@@ -95,11 +111,29 @@ def _stamp_path() -> str:
     return os.path.join(BUILD, "digest.txt")
 
 
-def is_fresh() -> bool:
-    if not all(os.path.exists(p) for p in (LIB_PATH, CACHE_LIB_PATH, PAGED_LIB_PATH, PY_MODULE_PATH, _stamp_path())):
+def _module_stamp_path() -> str:
+    return os.path.join(BUILD, PY_MODULE + ".digest.txt")
+
+
+def _stamped(stamp: str, digest: str) -> bool:
+    if not os.path.exists(stamp):
         return False
-    with open(_stamp_path()) as fh:
-        return fh.read().strip() == source_digest()
+    with open(stamp) as fh:
+        return fh.read().strip() == digest
+
+
+def _libraries_fresh() -> bool:
+    return all(os.path.exists(p) for p in (LIB_PATH, CACHE_LIB_PATH, PAGED_LIB_PATH)) and \
+        _stamped(_stamp_path(), source_digest())
+
+
+def _module_fresh() -> bool:
+    """True also where no module can be built."""
+    return torch_with_cuda() is None or (os.path.exists(PY_MODULE_PATH) and _stamped(_module_stamp_path(), module_digest()))
+
+
+def is_fresh() -> bool:
+    return _libraries_fresh() and _module_fresh()
 
 
 def _compile(src: str, verbose: bool, build_dir: str, extra_flags) -> str:
@@ -117,8 +151,8 @@ def _compile(src: str, verbose: bool, build_dir: str, extra_flags) -> str:
 
 
 def _build_module(bdir: str) -> None:
-    """PY_SOURCE against this Python and its torch (found, not imported: that takes seconds)."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """PY_SOURCE against this Python and its torch."""
+    torch = torch_with_cuda()
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = PY_MODULE_PATH + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I" + INCLUDE,
@@ -132,6 +166,8 @@ def _build_module(bdir: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {PY_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PY_MODULE_PATH)
+    with open(_module_stamp_path(), "w") as fh:
+        fh.write(module_digest())
 
 
 def _link(objs, out: str, bdir: str) -> None:
@@ -147,33 +183,39 @@ def _link(objs, out: str, bdir: str) -> None:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str | None = None,
           build_dir: str | None = None) -> str:
-    """Compile and link the libraries unless they are already up to date. Returns the path
-    of the dense one.
+    """Compile and link the libraries unless they are already up to date, and the Python module.
+    Returns the path of the dense library.
 
     extra_flags / lib_path / build_dir build a separate copy of the dense library (e.g.
     with -D tile overrides for tuning) without touching the in-tree ones.
     """
     default = lib_path is None and not extra_flags
-    if default and not force and is_fresh():
-        return LIB_PATH
+    libraries = force or not default or not _libraries_fresh()
+    module = default and torch_with_cuda() is not None and (force or not _module_fresh())
     out = LIB_PATH if lib_path is None else lib_path
     bdir = BUILD if build_dir is None else build_dir
+    if not libraries and not module:
+        return out
     os.makedirs(bdir, exist_ok=True)
     sources = SOURCES + (CACHE_SOURCES + PAGED_SOURCES if default else [])
     with cf.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
-        module = ex.submit(_build_module, bdir) if default else None
-        objs = list(ex.map(lambda s: _compile(s, verbose, bdir, tuple(extra_flags)), sources))
-        if module:
-            module.result()
-    with open(os.path.join(bdir, "exports.map"), "w") as fh:
-        fh.write("{\n  global: fa2_*;\n  local: *;\n};\n")
-    _link(objs[:len(SOURCES)], out, bdir)
-    if default:
-        rest = objs[len(SOURCES):]
-        _link(rest[:len(CACHE_SOURCES)], CACHE_LIB_PATH, bdir)
-        _link(rest[len(CACHE_SOURCES):], PAGED_LIB_PATH, bdir)
-        with open(_stamp_path(), "w") as fh:
-            fh.write(source_digest())
+        # (beside the libraries, which do not wait for it nor fail with it)
+        done = ex.submit(_build_module, bdir) if module else None
+        if libraries:
+            objs = list(ex.map(lambda s: _compile(s, verbose, bdir, tuple(extra_flags)), sources))
+            with open(os.path.join(bdir, "exports.map"), "w") as fh:
+                fh.write("{\n  global: fa2_*;\n  local: *;\n};\n")
+            _link(objs[:len(SOURCES)], out, bdir)
+            if default:
+                rest = objs[len(SOURCES):]
+                _link(rest[:len(CACHE_SOURCES)], CACHE_LIB_PATH, bdir)
+                _link(rest[len(CACHE_SOURCES):], PAGED_LIB_PATH, bdir)
+                with open(_stamp_path(), "w") as fh:
+                    fh.write(source_digest())
+        if done:
+            done.result()
+    if default and torch_with_cuda() is None:
+        print(f"{PY_MODULE} is not built: there is no torch with CUDA (the C libraries need none)", file=sys.stderr)
     return out
 
 
