@@ -12,6 +12,8 @@
 // 5/3: 58.5, 7/4: 58.9; ragged steps, by columns, 1/1: 75, 2/1: 71, 3/1: 69; one short
 // sequence, 3/1: 9.3, 3/2: 10.1, 3/4: 11.9.
 // Lengths are device data, so every CTA lays out the line for itself.
+// (fa2_paged_line.cuh and fa2_paged_merge.cuh have Span, Line, line_grid, find_range and merge_row of the
+// 16-bit cache, which are much alike: what is mended in one is to be looked at in the other.)
 #pragma once
 
 #include "fa2_cache.cuh"

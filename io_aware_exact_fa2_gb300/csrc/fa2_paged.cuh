@@ -1,7 +1,6 @@
 // fa2_paged.cuh -- what the kernels of the 16-bit key/value cache and of the position rotation
 // (include/fa2_paged.h) share: argument blocks, tensor maps, bf16 and fp16 pairs.  The cache
-// itself is the 8-bit one's View without scales, and attention's arguments are its AttnArgs, so
-// that both take the same line of work (fa2_cache_line.cuh).
+// itself is the 8-bit one's View without scales, and attention's arguments are its AttnArgs.
 #pragma once
 
 #include <cstdint>
@@ -40,7 +39,6 @@ struct MoveArgs {                   // fa2_rope, fa2_paged_append
     Rotation r;
     const int *starts, *counts;     // may be null: 0, L
     int B, L, D;
-    int append;                     // rows past counts are not read
 };
 
 // A weight is 2^LIFT of the type where its score is the row's reference (a score up to 8 below its

@@ -10,6 +10,11 @@
 // to do with it.  No range is shorter than C::LEAST places (but a line that is), at least what a
 // grain takes: so each range that ends inside a unit's grains, or between two that do, holds the
 // first place of one of them.
+//
+// Of fa2_cache_line.cuh the sequences' lengths (Seq, sequence, row_blocks), the cut into ranges (Range),
+// the workspace (Parts) and LineShared are taken as they are.  Span, Line, line_grid and find_range stand
+// in both files, there in tiles, here in places and grains: what is mended in one is to be looked at
+// in the other.
 #pragma once
 
 #include "fa2_cache_line.cuh"

@@ -1,5 +1,7 @@
-// fa2_paged_merge.cuh -- the parts of a row whose keys several CTAs share (fa2_cache_line.cuh),
-// put together: fa2_paged_step.cuh and fa2_paged_chunk.cuh.
+// fa2_paged_merge.cuh -- the parts of a row whose keys several CTAs share (fa2_paged_line.cuh),
+// put together: fa2_paged_step.cuh and fa2_paged_chunk.cuh.  (The 8-bit cache's merge_row, in
+// fa2_cache_line.cuh, is this one with parts that carry their log2-sum-exp2 as two floats: what is
+// mended in one is to be looked at in the other.)
 //
 // A part says what it computed as O / l and two floats: M, a score as the products gave it, and
 // y = log2 of the sum of 2^((S - M) c).  Scores stay scores: a difference of two M times c is exact
