@@ -53,9 +53,9 @@ struct Weight {
     static constexpr float LIFT = F16 ? 6.f : -12.f, UNIT = F16 ? 64.f : 1.f / 4096;
 };
 
-// Blocks of a move, which a launch counts in an int.
+// Blocks of a move, which a launch counts in an int (of more only where there are few).
 long long move_blocks(const MoveArgs &a);
-fa2_status launch_move(const MoveArgs &a, bool f16, cudaStream_t stream);
+fa2_status launch_move(const MoveArgs &a, bool f16, int num_sms, cudaStream_t stream);
 // Head dimension D, 64, 128 or 256 (fa2_paged_attn_d*.cu).
 template <int D>
 fa2_status launch_attn(const AttnArgs &a, bool f16);

@@ -126,7 +126,10 @@ fa2_status move(MoveArgs &a, bool f16, const void *owner, void *stream)
     const Device dev(owner);
     if (dev.status() != FA2_OK)
         return dev.status();
-    return launch_move(a, f16, static_cast<cudaStream_t>(stream));
+    const int sms = fa2::sm_count(dev.id());
+    if (sms <= 0)
+        return FA2_ERR_CUDA;
+    return launch_move(a, f16, sms, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace

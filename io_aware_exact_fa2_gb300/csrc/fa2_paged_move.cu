@@ -25,11 +25,10 @@ namespace {
 constexpr int THREADS = 128;
 constexpr int BATCH = 4;      // heads whose loads are under way together
 // Heads of one kind a block, so many share a load of cos and sin, and fewer where there would be
-// fewer blocks than BLOCKS, four an SM: one token of 128 sequences, 48 heads of 128 in all, 3.4 us,
+// fewer than BLOCKS blocks an SM: one token of 128 sequences, 48 heads of 128 in all, 3.4 us,
 // 4.7 with 8.  (More a block or less, in large calls: 8 prompts' append 89.0 us, 95 with 16, 97 with 4;
-// 2432 instead of 608 blocks: a gradient of 3 x 501 tokens 8.8 us for 7.0.)
-constexpr int HEADS = 8;
-constexpr long long BLOCKS = 608;
+// 16 instead of 4 blocks an SM: a gradient of 3 x 501 tokens 8.8 us for 7.0.)
+constexpr int HEADS = 8, BLOCKS = 4;
 
 // (x, y) by (c, s): (x c - y s, x s + y c)
 __device__ __forceinline__ void turn(float &x, float &y, float c, float s)
@@ -169,29 +168,29 @@ long long groups_of(const MoveArgs &a, int heads)
     return n;
 }
 
-// Heads a block, and the blocks.
-long long blocks_of(const MoveArgs &a, int &heads)
+// Blocks of tokens.
+long long tokens_of(const MoveArgs &a)
 {
     const int per = THREADS >> lpr_shift_of(a.D);
-    const long long tokens = (static_cast<long long>(a.B) * a.L + per - 1) / per;   // (below 2^62)
-    heads = HEADS;
-    while (heads > 1 && tokens < BLOCKS && tokens * groups_of(a, heads) < BLOCKS)
-        heads /= 2;
-    return groups_of(a, heads) > INT_MAX / tokens ? 1ll << 40 : tokens * groups_of(a, heads);
+    return (static_cast<long long>(a.B) * a.L + per - 1) / per;   // (below 2^62)
 }
 
 }  // namespace
 
 long long move_blocks(const MoveArgs &a)
 {
-    int heads;
-    return static_cast<long long>(a.B) * a.L > INT_MAX ? 1ll << 40 : blocks_of(a, heads);
+    if (static_cast<long long>(a.B) * a.L > INT_MAX || groups_of(a, HEADS) > INT_MAX / tokens_of(a))
+        return 1ll << 40;
+    return tokens_of(a) * groups_of(a, HEADS);
 }
 
-fa2_status launch_move(const MoveArgs &a, bool f16, cudaStream_t stream)
+fa2_status launch_move(const MoveArgs &a, bool f16, int num_sms, cudaStream_t stream)
 {
-    int heads;
-    const int blocks = static_cast<int>(blocks_of(a, heads)), groups = static_cast<int>(groups_of(a, heads));
+    const long long tokens = tokens_of(a), wanted = static_cast<long long>(BLOCKS) * num_sms;
+    int heads = HEADS;
+    while (heads > 1 && tokens * groups_of(a, heads) < wanted)
+        heads /= 2;
+    const int blocks = static_cast<int>(tokens * groups_of(a, heads)), groups = static_cast<int>(groups_of(a, heads));
     if (f16)
         move_kernel<true><<<blocks, THREADS, 0, stream>>>(a, groups, heads, lpr_shift_of(a.D));
     else
