@@ -145,14 +145,15 @@ fa2_status fa2_paged_append(const fa2_paged *c, const void *k, const void *v, co
  * Scores, sums, softmax statistics and O are fp32, O rounded once to the cache's type.
  * For the product with V a softmax weight is rounded: up to 16 rows (Lq * Hq / H), up to
  * 32 for D of 64 and 128, and for bf16 at D of 256 whatever the rows, to two terms of the
- * cache's type together, off by 2^-16 of the weight for bf16 and 2^-22 for fp16 (or by 2^-31
- * of the row's largest weight, whichever is more); for more rows to one term, off by 2^-9
- * and 2^-12 on average and 2^-8 and 2^-11 at most.  For those bf16 O is divided by the sum of
- * the rounded weights (where one key dominates, its rounding cancels); LSE, and all else,
- * takes the sum before.
+ * cache's type together, off by 2^-16 of the weight for bf16 and 2^-22 for fp16; for more rows
+ * to one term, off by 2^-9 and 2^-12 on average and 2^-8 and 2^-11 at most.  An fp16 weight
+ * may in either case be off by 2^-31 of the row's largest weight, where that is more (so one
+ * below 2^-20 of it is held in fewer bits, and one below 2^-31 may count as 0); a bf16 one
+ * by 2^-114.  Where bf16 has one term O is divided by the sum of the rounded weights (where one
+ * key dominates, its rounding cancels); LSE, and all else, takes the sum before.
  * O is finite where values are, unless a column's sum_j exp(s_ij - max_j s_ij) |V_j| is 2^131
- * or more (for bf16 values of that size only: 8 keys alike of the largest finite value, any
- * number of 2^101).  A key's part in it counts down to 2^-137 (bf16).
+ * or more: not with 8 keys of the largest finite bf16 value, nor with any number of values
+ * below 2^101.  A bf16 key's part in it counts down to 2^-137.
  *
  *   q          16-bit [B, Hq, Lq, D] device view, strides (batch, head, row) or NULL.
  *   o          16-bit [B, Hq, Lq, D] device view (written), likewise; its rows must not

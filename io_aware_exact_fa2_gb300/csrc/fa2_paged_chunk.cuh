@@ -26,9 +26,11 @@
 // in fa2_paged_line.cuh.  A unit of 128 rows or fewer (D < 256) is a twin: its two row tiles are
 // the same rows with every other tile of keys each, put together at its end.
 //
-// Measured.  2048 tokens of a prompt over 16384 keys, theirs included, 32 and 8 heads of 128,
-// causal (515 GFLOP): 333 to 343 us, 1.50 to 1.55 PFLOP/s, 0.79 to 0.81 of the measured matrix
-// rate; the loop over tiles shifts by 3 % with any change of its code.  The same with heads of 64
+// Measured (in a graph, in bursts of some milliseconds at the full clock, 2070 MHz).  2048 tokens of a
+// prompt over 16384 keys, theirs included, 32 and 8 heads of 128, causal (515 GFLOP): 333 to 343 us,
+// 1.50 to 1.55 PFLOP/s, 0.79 to 0.81 of the measured matrix rate; for seconds, at the 1935 MHz that the
+// power cap leaves, 359 us, and 361 as calls from Python: the same cycles, 694 to 699 thousand.
+// The loop over tiles shifts by 3 % with any change of its code.  The same with heads of 64
 // (as many exponentials for half the products) 282 us; 16 and 4 heads of 256 478 us, fp16 384;
 // pages of 16 keys 347.  No single unit is the bound: in timing copies, without the exponentials 334 us for
 // 360, with half the bytes of K and V 341 for 354.
@@ -496,8 +498,8 @@ __global__ void __launch_bounds__(C::T, 1)
             __syncwarp();
         } else if (warp == C::WARP_LOAD || warp == C::WARP_V) {
             // ======================================== pages -> ring: keys' by one warp, values' by another
-            // (one warp for both: 570 us instead of 388 for the prompt chunk at D = 256, one term a weight, 391 instead of 346
-            // over pages of 16 at D = 128)
+            // (one warp for both: 570 us instead of 388 for the prompt chunk at D = 256, there with one term a
+            // weight, 391 instead of 346 over pages of 16 at D = 128)
             const bool values = warp == C::WARP_V;
             const CUtensorMap *const map = values ? &v_map : &k_map;
             volatile uint32_t *const info = sh_info + (values ? C::RING : 0);
@@ -925,7 +927,8 @@ __global__ void __launch_bounds__(C::T, 1)
             const float inv = l_seen == 0.f ? 0.f : 1.f / l_seen;
             // log2 of the weights' sum, relative to M c itself
             const float y = l == 0.f ? -INFINITY
-                                     : lg2_approx(l * (1.f / Weight<F16>::UNIT)) - (fabsf(reference<C>(M, c)) > LARGE ? 0.f : left_out<C>(M, c));
+                                     : lg2_approx(l * (1.f / Weight<F16>::UNIT)) -
+                                           (fabsf(reference<C>(M, c)) > LARGE ? 0.f : left_out<C>(M, c));
             const Row at = this_row();
             uint16_t *const o = static_cast<uint16_t *>(a.o) + line.b * a.o_sb;
             const long long o_place = at.live ? at.hq * a.o_sh + at.tok * a.o_sl : -1;

@@ -8,10 +8,11 @@
 // much as a head's own traffic).  Pairs (j, R + j) are eight numbers at 8 c and eight at R + 8 c,
 // so no pair is split between threads, and rows may be turned in place.
 //
-// Measured (several inputs in turn, so that none is in L2): queries and keys of a training batch, 4 x
-// 8192 tokens, 32 and 8 heads of 128, 675 MB in 100 us, 6.7 TB/s; eight prompts of up to 4096
-// tokens appended, 607 MB in 89 us, 6.8 TB/s: 99 and 100 % of the measured copy rate.  Short calls are
-// a launch and three ways to memory, counts, page and rows: 2.6 us for 3 x 333 tokens.
+// Measured (several inputs in turn, so that none is in L2; in a graph, and as calls one after the
+// other): queries and keys of a training batch, 4 x 8192 tokens, 32 and 8 heads of 128, 675 MB in 101 us
+// (103), 6.7 TB/s; eight prompts of up to 4096 tokens appended, 607 MB in 89 to 92 us (94), 6.6 to 6.8
+// TB/s: 97 to 100 % of the measured copy rate (calls: 97 and 95).  Short calls are a launch and three
+// ways to memory, counts, page and rows: 2.6 to 2.8 us (4.1) for 3 x 333 tokens.
 #include <climits>
 
 #include "fa2_paged.cuh"

@@ -27,7 +27,8 @@
 // to 16 rows two CTAs share an SM and hide each other's beginnings and ends; 17 to 32 take two
 // groups of four softmax warps, half of the rows each, in one CTA with twice the ring.
 //
-// Measured.  One token of 40 sequences of up to 10000 keys, 32 and 8 heads of 128: 824 MB in
+// Measured (in a graph; calls from Python, one after the other, take 2 us more).  One token of 40
+// sequences of up to 10000 keys, 32 and 8 heads of 128: 824 MB in
 // 126 us, 6.5 TB/s, 0.96 of the measured copy rate; two of up to 131072 keys 946 MB in 141 us, 0.99;
 // 16 of 6000 keys with heads of 64 197 MB in 39 us (their tiles are half as many bytes for the same
 // softmax); 8 of 8000 with heads of 256 525 MB in 86 us.  One short context is 8.2 to 8.6 us: a
