@@ -77,9 +77,9 @@ struct ChunkCfg {
     // of bf16: six ragged prompts' chunks at D = 64 66 us with it, 59 without).
     static constexpr bool SEEN = !F16 && D < 256;
     // bf16 weights at D = 256 are two terms, as in the dense pass: with one, where two or three keys stand
-    // out alike, 9 of 8.2 M values around 2.3 were off by more than 1e-2 (2 x 8 heads, 2000 rows of 3000 keys,
-    // every 64th of them eight times as large), with two none but by their own rounding.  It costs one more
-    // product: the prompt chunk at D = 256 478 us, 388 with one (fp16, which has one, 384).
+    // out alike, 50 of 8.2 M values were off by more than 1e-2 (2 x 8 heads, 2000 rows of 3000 keys, every 64th
+    // of them eight times as large), some of 2 to 3, which no rounding of O explains; with two 41, all of 4 or
+    // more, whose own rounding it is.  It costs one more product: the prompt chunk at D = 256 478 us, 388 with one (fp16, which has one, 384).
     static constexpr bool TWO = !F16 && D == 256;
     static constexpr float LIFT = Weight<F16>::LIFT;
 
