@@ -79,7 +79,8 @@ struct ChunkCfg {
     // bf16 weights at D = 256 are two terms, as in the dense pass: with one, where two or three keys stand
     // out alike, 50 of 8.2 M values were off by more than 1e-2 (2 x 8 heads, 2000 rows of 3000 keys, every 64th
     // of them eight times as large), some of 2 to 3, which no rounding of O explains; with two 41, all of 4 or
-    // more, whose own rounding it is.  It costs one more product: the prompt chunk at D = 256 478 us, 388 with one (fp16, which has one, 384).
+    // more, whose own rounding it is.  It costs one more product: the prompt chunk at D = 256 478 us, 388 with
+    // one (fp16, which has one, 384).
     static constexpr bool TWO = !F16 && D == 256;
     static constexpr float LIFT = Weight<F16>::LIFT;
 
